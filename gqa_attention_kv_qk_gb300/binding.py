@@ -43,7 +43,8 @@ class UaaAttnDesc(ctypes.Structure):
                 ("softcap", ctypes.c_float), ("has_sink", ctypes.c_int32),
                 ("kv_dtype", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
-                ("norm_offset", ctypes.c_int32), ("reproducible", ctypes.c_int32)]
+                ("norm_offset", ctypes.c_int32), ("reproducible", ctypes.c_int32),
+                ("first_tokens", ctypes.c_int32)]
 
 
 class UaaStepArgs(ctypes.Structure):
@@ -256,6 +257,7 @@ def make_desc(cfg: dict) -> UaaAttnDesc:
     d.rotary_dim = int(cfg.get("rotary_dim", 0) or 0)
     d.norm_offset = int(bool(cfg.get("norm_offset", False)))
     d.reproducible = int(bool(cfg.get("reproducible", False)))
+    d.first_tokens = int(cfg.get("first_tokens", 0) or 0)
     return d
 
 

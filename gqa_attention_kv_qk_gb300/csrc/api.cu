@@ -90,6 +90,7 @@ uaa_status check_desc(const uaa_attn_desc* d)
     if (d->qk_norm && (!(d->norm_eps >= 0.f) || !isfinite(d->norm_eps)))
         return fail(UAA_ERR_UNSUPPORTED, "norm_eps=%g is not a finite value >= 0", (double)d->norm_eps);
     if (d->window < 0) return fail(UAA_ERR_UNSUPPORTED, "window=%d is negative", d->window);
+    if (d->first_tokens < 0) return fail(UAA_ERR_UNSUPPORTED, "first_tokens=%d is negative", d->first_tokens);
     if (!(d->softcap >= 0.f) || !isfinite(d->softcap))
         return fail(UAA_ERR_UNSUPPORTED, "softcap=%g is not a finite value >= 0", (double)d->softcap);
     if (d->has_sink != 0 && d->has_sink != 1)
@@ -299,6 +300,18 @@ uaa_status prepare(const uaa_attn_desc* d, const uaa_step_args* a, const uaa_wor
     return UAA_OK;
 }
 
+// The partition covers the union of the rows' windows: the first token's window
+// starts q_len - 1 keys before the last one's. A window that no position reaches
+// (2^31 keys with the chunk) is none.
+int partition_window(const uaa_attn_desc* d, const Plan& pl)
+{
+    const long long w = (long long)d->window + pl.q_len - 1;
+    return d->window > 0 && w <= 2147483647LL ? (int)w : 0;
+}
+
+// The keys that stay visible behind the window; without a window every key is.
+int first_tokens(const uaa_attn_desc* d) { return d->window > 0 ? d->first_tokens : 0; }
+
 float softmax_scale(const uaa_attn_desc* d)
 {
     return d->scale > 0.f ? d->scale : 1.0f / sqrtf((float)d->head_dim);
@@ -484,6 +497,7 @@ uaa_status run_prefill(const uaa_attn_desc* d, const uaa_step_args* a, const uaa
     p.q_len = pl.q_len;
     p.cap = a->cache_capacity;
     p.window = d->window;
+    p.first_tokens = first_tokens(d);
     p.softcap_log2e = d->softcap > 0.f ? d->softcap * uaa::kLog2e : 0.f;
     p.q_prime = reinterpret_cast<const float*>(w + pl.off_qrot);
     p.seq_lens = a->seq_lens;
@@ -571,9 +585,8 @@ uaa_status run_partial(const uaa_attn_desc* d, const uaa_step_args* a, const uaa
         p.cap = a->cache_capacity;
         p.q_len = pl.q_len;
         p.attn_window = d->window;
-        // the partition covers the union of the rows' windows: the first token's
-        // window starts q_len - 1 keys before the last one's
-        p.window = d->window > 0 ? d->window + pl.q_len - 1 : 0;
+        p.window = partition_window(d, pl);
+        p.first_tokens = first_tokens(d);
         p.mg = pl.mg;
         p.softcap_log2e = d->softcap > 0.f ? d->softcap * uaa::kLog2e : 0.f;
         p.q_prime = reinterpret_cast<const float*>(w + pl.off_qrot) + (size_t)b0 * pl.q_len * Hq * D;
@@ -648,7 +661,7 @@ uaa_status run_combine(const uaa_attn_desc* d, const uaa_step_args* a, const uaa
         p.heads_per_cta = pl.heads_per_cta;
         p.head_groups = pl.head_groups;
         p.q_len = pl.q_len;
-        p.window = d->window > 0 ? d->window + pl.q_len - 1 : 0;
+        p.window = partition_window(d, pl);
         p.mg = pl.mg;
         p.P = pl.n_ctas;
         p.out_dtype = d->out_dtype;
@@ -703,6 +716,7 @@ uaa_status run_step_f32(const uaa_attn_desc* d, const uaa_step_args* a, const ua
     p.cap = a->cache_capacity;
     p.max_len = a->max_seq_len;
     p.window = d->window;
+    p.first_tokens = first_tokens(d);
     p.splits = splits;
     p.split_keys = kF32SplitKeys;
     p.style = d->rope.style;

@@ -118,6 +118,7 @@ struct PartialParams {
     int head_groups;        // row groups per kv head: ceil(q_len G / heads_per_cta)
     int q_len;              // tokens per sequence: a unit's rows are (token, head) pairs (query_row)
     int attn_window;        // the descriptor's window (0: none), per query row
+    int first_tokens;       // keys of a sequence that stay visible behind the window (0 without one)
     int cap, window;        // window: of the partition, attn_window + q_len - 1 (0: none)
     int mg;                 // 64-key tiles per stage
     float softcap_log2e;    // 0: no softcap; else softcap * log2(e)
@@ -189,6 +190,7 @@ struct StepF32Params {
     int head_groups;        // ceil(G / 8)
     int cap, max_len;
     int window;             // the descriptor's window (0: none)
+    int first_tokens;       // keys that stay visible behind it (0 without a window)
     int splits;             // key splits per unit: each split_keys keys, the last takes the rest
     int split_keys;
     int style, half_rot, qk_norm;
@@ -224,6 +226,7 @@ struct PrefillParams {
     int q_len;              // tokens per sequence
     int cap;
     int window;             // the descriptor's window per query row (0: none)
+    int first_tokens;       // keys that stay visible behind it (0 without a window)
     float softcap_log2e;    // 0: no softcap; else softcap * log2(e)
     const float* q_prime;   // [B][q_len][Hq][D], written by the append
     const int* seq_lens;    // lengths after the append
@@ -248,6 +251,9 @@ struct PartialMaps {
 };
 cudaError_t launch_partial_tc(const PartialParams& p, const PartialMaps& m, int kv_dtype, int n_head_tiles,
                               int n_ctas, cudaStream_t s);
+// The same for launches with first tokens behind a window (partial_tc_first.cu; launch_partial_tc calls it).
+cudaError_t launch_partial_tc_first(const PartialParams& p, const PartialMaps& m, int kv_dtype, int n_head_tiles,
+                                    int n_ctas, cudaStream_t s);
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t s);
 // tk, tv: tensor maps of the key and value caches with boxes of kPrefillKeys rows x 64 columns.
 cudaError_t launch_prefill_umma(const PrefillParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
@@ -315,20 +321,54 @@ __device__ __forceinline__ void store_out(void* out, int dtype, size_t i, float 
         static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
 }
 
-// Visible keys of a sequence holding n keys after the append: [lo, n) with a
-// window W keeping the last W of them (positions j > pos - W, pos = n - 1).
-__host__ __device__ inline void key_range(int n, int window, int& lo, int& hi)
+// The keys a unit's rows see: [0, first) and [lo, hi), first <= lo. With a
+// window W over n keys the run [lo, hi) is the last W of them (positions
+// j > pos - W, pos = n - 1); the first F tokens of the sequence stay visible
+// behind it. Where they reach the window (F >= lo) the two are one run, lo = 0
+// and first = 0; so first > 0 says that keys are left out between the two.
+struct Keys {
+    int lo, hi, first;
+};
+
+__host__ __device__ inline Keys key_range(int n, int window, int first_tokens)
 {
-    hi = n;
-    lo = (window > 0 && n > window) ? n - window : 0;
+    Keys k;
+    k.hi = n;
+    k.lo = (window > 0 && n > window) ? n - window : 0;
+    k.first = k.lo > first_tokens ? first_tokens : 0;
+    if (k.lo <= first_tokens) k.lo = 0;
+    return k;
 }
 
-// Ring stages (mg tiles of 64 keys each) covering tiles [lo / 64, ceil(hi / 64)).
-__host__ __device__ inline int stages_of(int lo, int hi, int mg)
+// Ring stages (mg tiles of 64 keys each) that cover [0, first) ...
+__host__ __device__ inline int first_stages_of(const Keys& k, int mg)
 {
-    if (hi <= lo) return 0;
-    const int t0 = lo / kTileKeys, t1 = (hi + kTileKeys - 1) / kTileKeys;
-    return (t1 - t0 + mg - 1) / mg;
+    return (k.first + kTileKeys * mg - 1) / (kTileKeys * mg);
+}
+
+// ... and all of the unit's: those, then tiles [lo / 64, ceil(hi / 64)). The two
+// runs are cut into stages apart (a tile that both reach is loaded for each, its
+// keys masked by the run), so a stage is one contiguous piece of the cache.
+__host__ __device__ inline int stages_of(const Keys& k, int mg)
+{
+    if (k.hi <= k.lo) return 0;
+    const int t0 = k.lo / kTileKeys, t1 = (k.hi + kTileKeys - 1) / kTileKeys;
+    return first_stages_of(k, mg) + (t1 - t0 + mg - 1) / mg;
+}
+
+// Stage st of a unit whose first nf stages cover [0, first): its first key, and
+// the run [lo, hi) that its visible keys lie in. t0: the first tile of [lo, hi).
+struct StageKeys {
+    int key0, lo, hi;
+};
+
+// (FIRST: the launch keeps first tokens behind a window; without them nf is 0.)
+template <bool FIRST>
+__device__ __forceinline__ StageKeys stage_keys(const Keys& k, int t0, int nf, int st, int mg)
+{
+    if (FIRST && st < nf) return {mg * st * kTileKeys, 0, k.first};
+    if (!FIRST) nf = 0;
+    return {(t0 + mg * (st - nf)) * kTileKeys, k.lo, k.hi};
 }
 
 __host__ __device__ inline int record_of(int c, int cA, bool first_is_slot0)
@@ -349,19 +389,20 @@ __host__ __device__ inline int cta_of(long long x, long long T, int P)
     return static_cast<int>(((x + 1) * P + T - 1) / T) - 1;
 }
 
-// Visible keys [lo, hi) of sequence b, clamped to the cache (a longer length is
+// Visible keys of a sequence of n keys, clamped to the cache (a longer length is
 // flagged by the caller).
-__device__ __forceinline__ void visible_keys(int n, int window, int cap, int& lo, int& hi)
+__device__ __forceinline__ Keys visible_keys(int n, int window, int first_tokens, int cap)
 {
-    key_range(n, window, lo, hi);
-    if (hi > cap) hi = cap;
+    Keys k = key_range(n, window, first_tokens);
+    if (k.hi > cap) k.hi = cap;
+    return k;
 }
 
 // Keys that the partial kernel attends for a sequence holding L keys: with the
 // fused append the new token (slot L) is included when it fits the cache.
-__device__ __forceinline__ void sequence_keys(int L, int window, int cap, bool fused, int& lo, int& hi)
+__device__ __forceinline__ Keys sequence_keys(int L, int window, int first_tokens, int cap, bool fused)
 {
-    visible_keys(fused && L >= 0 && L < cap ? L + 1 : L, window, cap, lo, hi);
+    return visible_keys(fused && L >= 0 && L < cap ? L + 1 : L, window, first_tokens, cap);
 }
 
 // Block-wide prefix[0..B] of units * stages per sequence into shared memory, and
@@ -371,8 +412,8 @@ __device__ __forceinline__ void sequence_keys(int L, int window, int cap, bool f
 // With `owners` (one CTA of the launch passes it) the owner words of the units
 // of a sequence without stages are zeroed: no range writes them, and the
 // workspace region may hold other data from a step of another geometry.
-__device__ inline void build_stage_prefix(const int* seq_lens, int B, int window, int cap, int mg, int units,
-                                          int* prefix, int* lens, int* global_copy, unsigned* status,
+__device__ inline void build_stage_prefix(const int* seq_lens, int B, int window, int first_tokens, int cap, int mg,
+                                          int units, int* prefix, int* lens, int* global_copy, unsigned* status,
                                           bool fused = false, int max_len = 0, unsigned* owners = nullptr)
 {
     if (threadIdx.x < 32) {
@@ -390,9 +431,7 @@ __device__ inline void build_stage_prefix(const int* seq_lens, int B, int window
                 lens[b] = n;
                 if (status && (fused ? (n < 0 || n >= cap) : n > cap)) atomicOr(status, UAA_DEVFLAG_CAPACITY);
                 if (status && fused && n >= 0 && n < cap && n > max_len) atomicOr(status, UAA_DEVFLAG_LEN_HINT);
-                int lo, hi;
-                sequence_keys(n, window, cap, fused, lo, hi);
-                v = units * stages_of(lo, hi, mg);
+                v = units * stages_of(sequence_keys(n, window, first_tokens, cap, fused), mg);
                 if (owners && v == 0)
                     for (int u = 0; u < 2 * units; ++u) owners[2 * static_cast<size_t>(b) * units + u] = 0u;
             }
@@ -430,13 +469,14 @@ struct Segment {
     int st0;        // first stage within the unit
     int n_st;       // stages in the segment
     int stages;     // stages of the whole unit
-    int lo, hi;     // visible keys of the sequence
+    Keys keys;      // visible keys of the sequence
+    int nf;         // the unit's first nf stages cover keys [0, keys.first)
     bool whole;     // the segment is the whole unit
 };
 
-__device__ __forceinline__ Segment segment_at(const int* prefix, const int* lens, int B, int window, int cap,
-                                              int head_groups, int units, long long pos, long long end,
-                                              bool fused = false)
+__device__ __forceinline__ Segment segment_at(const int* prefix, const int* lens, int B, int window, int first_tokens,
+                                              int cap, int mg, int head_groups, int units, long long pos,
+                                              long long end, bool fused = false)
 {
     Segment sg;
     sg.b = find_sequence(prefix, B, pos);
@@ -449,7 +489,8 @@ __device__ __forceinline__ Segment segment_at(const int* prefix, const int* lens
     sg.n_st = left < sg.stages - sg.st0 ? static_cast<int>(left) : sg.stages - sg.st0;
     sg.kvh = u / head_groups;
     sg.hg = u - sg.kvh * head_groups;
-    sequence_keys(lens[sg.b], window, cap, fused, sg.lo, sg.hi);
+    sg.keys = sequence_keys(lens[sg.b], window, first_tokens, cap, fused);
+    sg.nf = first_stages_of(sg.keys, mg);
     sg.whole = sg.st0 == 0 && sg.n_st == sg.stages;
     return sg;
 }

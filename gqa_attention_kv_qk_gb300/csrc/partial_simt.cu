@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) partial_simt_kernel(const Par
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int units = p.Hkv * p.head_groups;
     grid_dependency_wait();  // the append's lengths, q rows and cache rows are complete
-    build_stage_prefix(p.seq_lens, p.B, p.window, p.cap, 1, units, prefix, lens,
+    build_stage_prefix(p.seq_lens, p.B, p.window, p.first_tokens, p.cap, 1, units, prefix, lens,
                        blockIdx.x == 0 ? p.prefix : nullptr, blockIdx.x == 0 ? p.status : nullptr, false, 0,
                        blockIdx.x == 0 ? p.owners : nullptr);
     const long long T = prefix[p.B];
@@ -48,11 +48,13 @@ __global__ void __launch_bounds__(kSimtWarps * 32) partial_simt_kernel(const Par
     }
 
     for (long long pos = s_c; pos < e_c;) {
-        const Segment sg = segment_at(prefix, lens, p.B, p.window, p.cap, p.head_groups, units, pos, e_c);
+        const Segment sg = segment_at(prefix, lens, p.B, p.window, p.first_tokens, p.cap, 1, p.head_groups, units, pos,
+                                      e_c);
         const int r0 = sg.hg * kSimtHeads;                   // the unit's first query row (query_row)
         const int nh = min(kSimtHeads, p.q_len * p.G - r0);  // its query rows
         // several tokens per sequence: row r (token r / G) sees keys up to its own
         // position, lens[b] - q_len + r / G, and with a window the last attn_window
+        // and the first first_tokens
         int kmax[kSimtHeads], kmin[kSimtHeads];
 #pragma unroll
         for (int h = 0; h < kSimtHeads; ++h) {
@@ -64,9 +66,6 @@ __global__ void __launch_bounds__(kSimtWarps * 32) partial_simt_kernel(const Par
             if (sg.st0 == 0) own[0] = (blockIdx.x + 1u) | (pos == s_c ? 0x80000000u : 0u);
             if (sg.st0 + sg.n_st == sg.stages) own[1] = blockIdx.x + 1u;
         }
-        const int t0 = sg.lo / kTileKeys;
-        const int j_beg = max(sg.lo, (t0 + sg.st0) * kTileKeys);
-        const int j_end = min(sg.hi, (t0 + sg.st0 + sg.n_st) * kTileKeys);
 
         float q[kSimtHeads][EPL];
 #pragma unroll
@@ -89,6 +88,14 @@ __global__ void __launch_bounds__(kSimtWarps * 32) partial_simt_kernel(const Par
         const float* V = static_cast<const float*>(p.v_cache);
         // warp w takes blocks of KB consecutive keys round-robin; a block's rows are
         // all loaded before the first is used (one memory round trip per block)
+        // (the segment's stages of the first tokens, then those of [lo, hi))
+        for (int run = 0; run < 2; ++run) {
+        const int s0 = run == 0 ? sg.st0 : max(sg.st0, sg.nf);
+        const int s1 = run == 0 ? min(sg.st0 + sg.n_st, sg.nf) : sg.st0 + sg.n_st;
+        if (s0 >= s1) continue;
+        const StageKeys sk = stage_keys<true>(sg.keys, sg.keys.lo / kTileKeys, sg.nf, s0, 1);
+        const int j_beg = max(sk.lo, sk.key0);
+        const int j_end = min(sk.hi, sk.key0 + (s1 - s0) * kTileKeys);
         for (int jb = j_beg + warp * KB; jb < j_end; jb += kSimtWarps * KB) {
             float kx[KB][EPL], vx[KB][EPL];
 #pragma unroll
@@ -109,7 +116,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) partial_simt_kernel(const Par
 #pragma unroll
                 for (int h = 0; h < kSimtHeads; ++h) {
                     if (h >= nh) break;
-                    if (jb + u > kmax[h] || jb + u < kmin[h]) continue;  // beyond the row's own token
+                    if (jb + u > kmax[h] || (jb + u < kmin[h] && jb + u >= p.first_tokens)) continue;  // beyond the row's own token
                     float dot = 0.f;
 #pragma unroll
                     for (int i = 0; i < EPL; ++i) dot = fmaf(q[h][i], kx[u][i], dot);
@@ -124,6 +131,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) partial_simt_kernel(const Par
                     m[h] = mn;
                 }
             }
+        }
         }
 
         __syncthreads();  // the previous segment's merge reads are done

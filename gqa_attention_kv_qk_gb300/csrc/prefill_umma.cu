@@ -98,7 +98,8 @@ __device__ __forceinline__ void um_split_trunc(float x0, float x1, uint32_t& hi,
     lo = __byte_perm(__float_as_uint(x0 - __uint_as_float(h0)), __float_as_uint(x1 - __uint_as_float(h1)), 0x7632);
 }
 
-template <int D>
+// FIRST: the launch keeps first tokens behind a window (PrefillParams.first_tokens).
+template <int D, bool FIRST>
 __global__ void __launch_bounds__(kUmThreads, 1)
 prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const PrefillParams p)
@@ -170,10 +171,17 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const int L = L_after - p.q_len;
     const bool valid = L >= 0 && L_after <= p.cap;
     const int r_first = rb * kUmRows, r_last = min(rows, r_first + kUmRows) - 1;
-    const int hi = valid ? L + r_last / p.G + 1 : 0;  // keys the block sees: [lo, hi)
-    const int lo = valid && p.window > 0 ? max(0, L + r_first / p.G + 1 - p.window) : 0;
+    // keys the block sees: [0, first) and [lo, hi) (Keys), in n_f and n_st - n_f key
+    // blocks; block j starts at key block_key(j) and its keys lie in the run of its part
+    const int hi = valid ? L + r_last / p.G + 1 : 0;
+    const int lo_w = valid && p.window > 0 ? max(0, L + r_first / p.G + 1 - p.window) : 0;
+    const int first_tokens = FIRST ? p.first_tokens : 0;
+    const int first = lo_w > first_tokens ? first_tokens : 0;
+    const int lo = lo_w > first_tokens ? lo_w : 0;
+    const int n_f = FIRST ? (first + kUmKeys - 1) / kUmKeys : 0;
     const int kb0 = lo / kUmKeys;
-    const int n_st = (hi + kUmKeys - 1) / kUmKeys - kb0;  // key blocks
+    const int n_st = n_f + (hi + kUmKeys - 1) / kUmKeys - kb0;  // key blocks
+    auto block_key = [&](int j) { return (j < n_f ? j : kb0 + j - n_f) * kUmKeys; };
 
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producers
@@ -184,7 +192,7 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const uint32_t ring = is_v ? vring : kring;
             const uint32_t full = is_v ? bar_vfull : bar_kfull, empty = is_v ? bar_vempty : bar_kempty;
             const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
-            const int row0 = (b * p.Hkv + kvh) * p.cap + kb0 * kUmKeys;
+            const int row0 = (b * p.Hkv + kvh) * p.cap;
             int issued = 0;
             for (int i = 0; i < n_st; ++i) {
                 const int s = i % NSL;
@@ -196,7 +204,7 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 ptx::mbar_arrive_expect_tx(bar, SH::kTile);
 #pragma unroll
                 for (int c = 0; c < SH::kBoxes; ++c)  // plain loads: the other row blocks read the same tiles from L2
-                    ptx::tma_load_2d(st + c * (kUmKeys * 128), tm, c * 64, row0 + i * kUmKeys, bar);
+                    ptx::tma_load_2d(st + c * (kUmKeys * 128), tm, c * 64, row0 + block_key(i), bar);
                 issued = i + 1;
             }
             // every issued copy lands before the CTA may exit
@@ -327,16 +335,21 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             ptx::tc_fence_before();
             ptx::mbar_arrive(bar_sfree);  // the S buffer may be overwritten
 
-            const int key0 = (kb0 + j) * kUmKeys + KH * h;  // this thread's first key
+            const int key0 = block_key(j) + KH * h;  // this thread's first key
             if (cap2 > 0.f) {
 #pragma unroll
                 for (int i = 0; i < KH; ++i) x[i] = tanhf(x[i]) * cap2;
             }
-            if (!(row_ok && key0 + KH - 1 <= kmax && key0 >= kmin)) {  // some keys masked
-                const int i_lo = !row_ok ? KH : (p.window > 0 ? kmin - key0 : 0), i_hi = row_ok ? kmax - key0 : -1;
+            if (!(row_ok && key0 + KH - 1 <= kmax && (j < n_f ? key0 + KH <= first : key0 >= kmin))) {  // some keys masked
+                // keys below i_f are among the first tokens: visible in their own blocks, or
+                // where there is one run (not in the window's first block, which may hold
+                // them once more)
+                const int i_f = j < n_f || n_f == 0 ? first_tokens - key0 : INT_MIN;
+                const int i_lo = !row_ok ? KH : (p.window > 0 ? (j < n_f ? KH : kmin - key0) : 0);
+                const int i_hi = row_ok ? kmax - key0 : -1;
 #pragma unroll
                 for (int i = 0; i < KH; ++i)
-                    if (i < i_lo || i > i_hi) x[i] = -INFINITY;
+                    if ((i < i_lo && (!FIRST || i >= i_f || !row_ok)) || i > i_hi) x[i] = -INFINITY;
             }
             float mh;
             {
@@ -380,16 +393,20 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             // value rows of keys at or past the sequence's end (unused slots, or another
             // head's rows) may hold anything, NaN included: zero them once they have
-            // landed, as P is 0 there
-            const int v_keep = L_after - (kb0 + j) * kUmKeys;
-            if (v_keep < kUmKeys) {
+            // landed, as P is 0 there. So may rows behind the first tokens or before the
+            // window, which no row of the block sees (v_skip: rows before the run's start).
+            const int v_keep = (j < n_f ? first : L_after) - block_key(j);
+            const int v_skip = FIRST && j >= n_f ? lo - block_key(j) : 0;
+            if (v_keep < kUmKeys || v_skip > 0) {
                 const int sv = j % NV;
                 ok = __all_sync(0xffffffffu,
                                 ok && ptx::mbar_wait(bar_vfull + 8 * sv, (j / NV) & 1, kWaitLimitCycles));
                 const uint32_t vt = vring + sv * SH::kTile;
-                const int first = max(v_keep, 0), n_chunks = (kUmKeys - first) * SH::kBoxes * 8;
+                const int tail = min(max(v_keep, 0), kUmKeys), head = max(v_skip, 0);
+                const int n_chunks = (head + kUmKeys - tail) * SH::kBoxes * 8;
                 for (int i = tid; i < n_chunks && ok; i += kUmSoftmax) {
-                    const int row = first + i / (SH::kBoxes * 8), rem = i % (SH::kBoxes * 8);
+                    const int rz = i / (SH::kBoxes * 8), rem = i % (SH::kBoxes * 8);
+                    const int row = rz < head ? rz : tail + rz - head;
                     ptx::st_shared_v4(vt + (rem >> 3) * (kUmKeys * 128) + row * 128 + (rem & 7) * 16, 0u, 0u, 0u, 0u);
                 }
                 ptx::fence_proxy_async();  // visible to the tensor core
@@ -490,12 +507,12 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     }
 }
 
-template <int D>
+template <int D, bool FIRST>
 cudaError_t launch_um(const PrefillParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s)
 {
     using SH = UmShape<D>;
     static_assert(SH::kSmemBytes <= 232448, "shared memory of the prefill kernel");
-    auto kern = prefill_umma_kernel<D>;
+    auto kern = prefill_umma_kernel<D, FIRST>;
     static int configured_device_mask = 0;  // bit per device that has the smem attribute set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -517,8 +534,8 @@ cudaError_t launch_um(const PrefillParams& p, const CUtensorMap& tk, const CUten
 cudaError_t launch_prefill_umma(const PrefillParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s)
 {
     switch (p.D) {
-    case 64: return launch_um<64>(p, tk, tv, s);
-    case 128: return launch_um<128>(p, tk, tv, s);
+    case 64: return p.first_tokens > 0 ? launch_um<64, true>(p, tk, tv, s) : launch_um<64, false>(p, tk, tv, s);
+    case 128: return p.first_tokens > 0 ? launch_um<128, true>(p, tk, tv, s) : launch_um<128, false>(p, tk, tv, s);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -73,7 +73,9 @@ __device__ __forceinline__ void lane_sums(float (&v)[N], int lane)
     butterfly_step<N / 16, 1>(v, lane);
 }
 
-template <int D, int NH, typename T>  // NH: query heads per unit (4 or 8); T: io element type
+// NH: query heads per unit (4 or 8); T: io element type; FIRST: first tokens stay
+// visible behind the window (as a run-time choice they cost the others 7 %)
+template <int D, int NH, typename T, bool FIRST>
 __global__ void __launch_bounds__(kStepThreads) step_f32_kernel(const StepF32Params p)
 {
     constexpr int EPL = D / 32;            // row elements per lane
@@ -112,11 +114,16 @@ __global__ void __launch_bounds__(kStepThreads) step_f32_kernel(const StepF32Par
     // ---- the length and the keys of this split
     const int L = p.seq_lens[b];  // read by every thread before the CTA counts in (below)
     const bool fits = L >= 0 && L < p.cap;
-    int lo, hi;
-    visible_keys(fits ? L + 1 : L, p.window, p.cap, lo, hi);
+    // This split takes ranks [k0, k1) of the visible keys. Rank i is position i, or
+    // with first tokens apart from the window (FIRST) the first keys.first ranks are
+    // those and the others lie skip positions further on.
+    const Keys keys = visible_keys(fits ? L + 1 : L, p.window, FIRST ? p.first_tokens : 0, p.cap);
+    const int skip = FIRST ? keys.lo - keys.first : 0;
+    const int lo = FIRST ? 0 : keys.lo, hi = FIRST ? max(keys.hi - skip, 0) : keys.hi;
+    auto position = [&](int rank) { return !FIRST || rank < keys.first ? rank : rank + skip; };
     const int k0 = min(hi, lo + s * p.split_keys);
     const int k1 = s == S - 1 ? hi : min(hi, lo + (s + 1) * p.split_keys);
-    const bool has_new = fits && k0 <= L && L < k1;  // the new key is among this split's keys
+    const bool has_new = fits && k0 <= L - skip && L - skip < k1;  // the new key is among this split's keys
 
     // the rows this CTA needs, loaded before anything waits on them
     float x[EPL];
@@ -234,13 +241,13 @@ __global__ void __launch_bounds__(kStepThreads) step_f32_kernel(const StepF32Par
     for (int h = 0; h < NH; ++h) o[h][0] = o[h][1] = o[h][2] = o[h][3] = 0.f;
     const float cap2 = p.softcap_log2e;
     for (int kc = k0; kc < k1; kc += CK) {
-        const int nk = min(CK, k1 - kc);  // the chunk: keys kc .. kc + nk - 1
+        const int nk = min(CK, k1 - kc);  // the chunk: ranks kc .. kc + nk - 1
         __syncthreads();  // the previous chunk's rows and weights are used up
         // the chunk's key and value rows into shared memory (a thread per float4 in
         // turn: coalesced 16-byte asynchronous copies); the new key's rows from its
         // staged rows; rows behind an out-of-pool page entry read as zeros
         for (int f = tid; f < nk * C4; f += kStepThreads) {
-            const int jj = f / C4, c4 = f - jj * C4, j = kc + jj;
+            const int jj = f / C4, c4 = f - jj * C4, j = position(kc + jj);
             float* kd = ks + jj * KSTR + 4 * c4;
             float* vd = vs + jj * KSTR + 4 * c4;
             if (has_new && j == L) {
@@ -401,10 +408,10 @@ __global__ void __launch_bounds__(kStepThreads) step_f32_kernel(const StepF32Par
     }
 }
 
-template <int D, int NH, typename T>
+template <int D, int NH, typename T, bool FIRST>
 cudaError_t launch_step(const StepF32Params& p, dim3 grid, cudaStream_t s)
 {
-    auto kern = step_f32_kernel<D, NH, T>;
+    auto kern = step_f32_kernel<D, NH, T, FIRST>;
     static int configured_device_mask = 0;  // bit per device that has the smem attribute set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -421,7 +428,9 @@ template <int D, typename T>
 cudaError_t launch_heads(const StepF32Params& p, dim3 grid, cudaStream_t s)
 {
     // four query heads per kv head or fewer: every unit has at most 4 heads
-    return p.G <= 4 ? launch_step<D, 4, T>(p, grid, s) : launch_step<D, 8, T>(p, grid, s);
+    if (p.first_tokens > 0)
+        return p.G <= 4 ? launch_step<D, 4, T, true>(p, grid, s) : launch_step<D, 8, T, true>(p, grid, s);
+    return p.G <= 4 ? launch_step<D, 4, T, false>(p, grid, s) : launch_step<D, 8, T, false>(p, grid, s);
 }
 
 }  // namespace

@@ -150,7 +150,7 @@ typedef struct {
     uaa_rope_params rope;
     int32_t qk_norm;          /* 1: RMSNorm of each q and k head row before RoPE */
     float norm_eps;           /* RMSNorm epsilon, >= 0 */
-    int32_t window;           /* 0: none; W > 0: keys j with pos - W < j <= pos */
+    int32_t window;           /* 0: none; W > 0: keys j with pos - W < j <= pos (and first_tokens) */
     float softcap;            /* 0: none; c > 0: s -> c tanh(s / c), after the scale */
     int32_t has_sink;         /* 1: sink[h] joins the softmax denominator of head h */
     int32_t kv_dtype;         /* UAA_DTYPE_F32, _BF16, _VQ8 or _Q8 */
@@ -162,6 +162,11 @@ typedef struct {
     int32_t reproducible;     /* 1: the tensor-core partial step splits its ranges uniformly
                                  instead of by the slot speeds measured in earlier launches,
                                  so equal inputs give equal bits on every launch; else 0 */
+    int32_t first_tokens;     /* F >= 0: with a window W, keys j < F stay visible behind it, so a
+                                 token at pos sees j < F and pos - W < j <= pos (a stream that
+                                 keeps its first tokens). Keys keep the rotation of their own
+                                 positions. No effect without a window. Takes what was padding:
+                                 the struct's size and the other fields are unchanged */
 } uaa_attn_desc;
 
 typedef struct {
