@@ -25,7 +25,7 @@ UAA_DEVFLAG_PAGE = 0x8
 
 ROPE_STYLE = {"neox": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "llama3": 1, "yarn": 2, "linear": 3}
-DTYPE = {"f32": 0, "bf16": 1, "vq8": 2, "q8": 3}
+DTYPE = {"f32": 0, "bf16": 1, "vq8": 2, "q8": 3, "q4": 4}
 
 
 class UaaRopeParams(ctypes.Structure):
@@ -102,6 +102,12 @@ _SIGS = [
      [_P(UaaAttnDesc), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P(UaaWorkspaceLayout)]),
     ("uaa_vq8_quantize", ctypes.c_int,
      [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+      ctypes.c_void_p]),
+    ("uaa_q4_quantize", ctypes.c_int,
+     [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+      ctypes.c_void_p]),
+    ("uaa_cache_read", ctypes.c_int,
+     [_P(UaaAttnDesc), _P(UaaStepArgs), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
       ctypes.c_void_p]),
     ("uaa_device_status", ctypes.c_int, [_P(UaaWorkspace), ctypes.c_void_p, _P(ctypes.c_uint32)]),
     ("uaa_last_error", ctypes.c_char_p, []),
@@ -202,6 +208,20 @@ def uaa_vq8_quantize(v_ptr: int, v_dtype: int, n_rows: int, head_dim: int, codes
     return _check(lib().uaa_vq8_quantize(ctypes.c_void_p(v_ptr), v_dtype, n_rows, head_dim,
                                          ctypes.c_void_p(codes_ptr), ctypes.c_void_p(scales_ptr),
                                          _stream(stream)), check)
+
+
+def uaa_q4_quantize(x_ptr: int, x_dtype: int, n_rows: int, head_dim: int, codes_ptr: int, scales_ptr: int,
+                    stream=None, check=True) -> int:
+    return _check(lib().uaa_q4_quantize(ctypes.c_void_p(x_ptr), x_dtype, n_rows, head_dim,
+                                        ctypes.c_void_p(codes_ptr), ctypes.c_void_p(scales_ptr),
+                                        _stream(stream)), check)
+
+
+def uaa_cache_read(desc, args, start_ptr: int, n_rows: int, k_out_ptr: int, v_out_ptr: int, stream=None,
+                   check=True) -> int:
+    return _check(lib().uaa_cache_read(ctypes.byref(desc), ctypes.byref(args), ctypes.c_void_p(start_ptr), n_rows,
+                                       ctypes.c_void_p(k_out_ptr), ctypes.c_void_p(v_out_ptr), _stream(stream)),
+                  check)
 
 
 def uaa_device_status(ws, stream=None) -> int:

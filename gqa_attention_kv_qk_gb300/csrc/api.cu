@@ -96,8 +96,8 @@ uaa_status check_desc(const uaa_attn_desc* d)
     if (d->has_sink != 0 && d->has_sink != 1)
         return fail(UAA_ERR_UNSUPPORTED, "has_sink=%d is not 0 or 1", d->has_sink);
     if (d->kv_dtype != UAA_DTYPE_F32 && d->kv_dtype != UAA_DTYPE_BF16 && d->kv_dtype != UAA_DTYPE_VQ8 &&
-        d->kv_dtype != UAA_DTYPE_Q8)
-        return fail(UAA_ERR_UNSUPPORTED, "kv_dtype=%d is not F32, BF16, VQ8 or Q8", d->kv_dtype);
+        d->kv_dtype != UAA_DTYPE_Q8 && d->kv_dtype != UAA_DTYPE_Q4)
+        return fail(UAA_ERR_UNSUPPORTED, "kv_dtype=%d is not F32, BF16, VQ8, Q8 or Q4", d->kv_dtype);
     if (d->io_dtype != UAA_DTYPE_F32 && d->io_dtype != UAA_DTYPE_BF16)
         return fail(UAA_ERR_UNSUPPORTED, "io_dtype=%d is not F32 or BF16", d->io_dtype);
     if (d->out_dtype != UAA_DTYPE_F32 && d->out_dtype != UAA_DTYPE_BF16)
@@ -222,6 +222,63 @@ uaa_status make_plan(const uaa_attn_desc* d, int batch, int q_len, int max_len, 
     return UAA_OK;
 }
 
+// The facts of a step's caches: their geometry, and the pointers that hold them.
+uaa_status check_cache_shape(const uaa_attn_desc* d, const uaa_step_args* a)
+{
+    if (a->block_table) {
+        const int ps = a->page_size;
+        if (ps < 16 || ps > 4096 || (ps & (ps - 1)) != 0)
+            return fail(UAA_ERR_UNSUPPORTED, "page_size=%d is not a power of two in [16, 4096]", ps);
+        // a page's scales are one TMA box of a stage; its shared-memory destination
+        // (4 bytes per key, or D / 16 for q4) must start on 128 bytes
+        if (ps < 32 && d->kv_dtype != UAA_DTYPE_F32 && d->kv_dtype != UAA_DTYPE_BF16)
+            return fail(UAA_ERR_UNSUPPORTED, "page_size=%d is below 32, the smallest page of a vq8 / q8 / q4 cache", ps);
+        if (a->pages_per_seq <= 0 || (long long)a->pages_per_seq * ps != a->cache_capacity)
+            return fail(UAA_ERR_INVALID_ARGUMENT,
+                        "cache_capacity=%d is not pages_per_seq=%d x page_size=%d", a->cache_capacity,
+                        a->pages_per_seq, ps);
+        if (a->n_pages <= 0) return fail(UAA_ERR_INVALID_ARGUMENT, "n_pages=%d is not positive", a->n_pages);
+        if ((long long)a->n_pages * d->n_kv_heads * ps > 2147483647LL - 2 * uaa::kTileKeys)
+            return fail(UAA_ERR_UNSUPPORTED, "n_pages*n_kv_heads*page_size=%lld exceeds 2^31 cache rows",
+                        (long long)a->n_pages * d->n_kv_heads * ps);
+        if (!aligned16(a->block_table)) return fail(UAA_ERR_INVALID_ARGUMENT, "block_table is not 16-byte aligned");
+    } else if ((long long)a->batch * d->n_kv_heads * a->cache_capacity > 2147483647LL - 2 * uaa::kTileKeys) {
+        return fail(UAA_ERR_UNSUPPORTED, "batch*n_kv_heads*cache_capacity=%lld exceeds 2^31 cache rows",
+                    (long long)a->batch * d->n_kv_heads * a->cache_capacity);
+    }
+    return UAA_OK;
+}
+
+bool scaled_values(const uaa_attn_desc* d)
+{
+    return d->kv_dtype == UAA_DTYPE_VQ8 || d->kv_dtype == UAA_DTYPE_Q8 || d->kv_dtype == UAA_DTYPE_Q4;
+}
+
+bool scaled_keys(const uaa_attn_desc* d) { return d->kv_dtype == UAA_DTYPE_Q8 || d->kv_dtype == UAA_DTYPE_Q4; }
+
+// A call that only reads the caches (uaa_cache_read).
+uaa_status check_cache(const uaa_attn_desc* d, const uaa_step_args* a)
+{
+    if (!a) return fail(UAA_ERR_INVALID_ARGUMENT, "args is NULL");
+    if (a->batch < 0) return fail(UAA_ERR_INVALID_ARGUMENT, "batch=%d is negative", a->batch);
+    if (a->cache_capacity <= 0 || a->cache_capacity % 4 != 0)
+        return fail(UAA_ERR_INVALID_ARGUMENT, "cache_capacity=%d is not a positive multiple of 4", a->cache_capacity);
+    UAA_TRY(check_cache_shape(d, a));
+    const struct {
+        const void* p;
+        const char* name;
+        bool needed;
+    } ptrs[] = {{a->k_cache, "k_cache", true},
+                {a->v_cache, "v_cache", true},
+                {a->v_scale, "v_scale", scaled_values(d)},
+                {a->k_scale, "k_scale", scaled_keys(d)}};
+    for (auto& e : ptrs) {
+        if (e.needed && !e.p && a->batch > 0) return fail(UAA_ERR_INVALID_ARGUMENT, "%s is NULL", e.name);
+        if (e.p && !aligned16(e.p)) return fail(UAA_ERR_INVALID_ARGUMENT, "%s is not 16-byte aligned", e.name);
+    }
+    return UAA_OK;
+}
+
 uaa_status check_args(const uaa_attn_desc* d, const uaa_step_args* a, const uaa_workspace* ws, bool need_io)
 {
     if (!a) return fail(UAA_ERR_INVALID_ARGUMENT, "args is NULL");
@@ -236,27 +293,7 @@ uaa_status check_args(const uaa_attn_desc* d, const uaa_step_args* a, const uaa_
     if ((long long)a->max_seq_len + q_len > a->cache_capacity)
         return fail(UAA_ERR_CAPACITY, "max_seq_len=%d + %d new token(s) does not fit cache_capacity=%d",
                     a->max_seq_len, q_len, a->cache_capacity);
-    if (a->block_table) {
-        const int ps = a->page_size;
-        if (ps < 16 || ps > 4096 || (ps & (ps - 1)) != 0)
-            return fail(UAA_ERR_UNSUPPORTED, "page_size=%d is not a power of two in [16, 4096]", ps);
-        // a page's scales are one TMA box of a stage; its shared-memory destination
-        // (4 bytes per key) must start on 128 bytes
-        if (ps < 32 && (d->kv_dtype == UAA_DTYPE_VQ8 || d->kv_dtype == UAA_DTYPE_Q8))
-            return fail(UAA_ERR_UNSUPPORTED, "page_size=%d is below 32, the smallest page of a vq8 / q8 cache", ps);
-        if (a->pages_per_seq <= 0 || (long long)a->pages_per_seq * ps != a->cache_capacity)
-            return fail(UAA_ERR_INVALID_ARGUMENT,
-                        "cache_capacity=%d is not pages_per_seq=%d x page_size=%d", a->cache_capacity,
-                        a->pages_per_seq, ps);
-        if (a->n_pages <= 0) return fail(UAA_ERR_INVALID_ARGUMENT, "n_pages=%d is not positive", a->n_pages);
-        if ((long long)a->n_pages * d->n_kv_heads * ps > 2147483647LL - 2 * uaa::kTileKeys)
-            return fail(UAA_ERR_UNSUPPORTED, "n_pages*n_kv_heads*page_size=%lld exceeds 2^31 cache rows",
-                        (long long)a->n_pages * d->n_kv_heads * ps);
-        if (!aligned16(a->block_table)) return fail(UAA_ERR_INVALID_ARGUMENT, "block_table is not 16-byte aligned");
-    } else if ((long long)a->batch * d->n_kv_heads * a->cache_capacity > 2147483647LL - 2 * uaa::kTileKeys) {
-        return fail(UAA_ERR_UNSUPPORTED, "batch*n_kv_heads*cache_capacity=%lld exceeds 2^31 cache rows",
-                    (long long)a->batch * d->n_kv_heads * a->cache_capacity);
-    }
+    UAA_TRY(check_cache_shape(d, a));
     struct {
         const void* p;
         const char* name;
@@ -269,8 +306,8 @@ uaa_status check_args(const uaa_attn_desc* d, const uaa_step_args* a, const uaa_
         {a->v_cache, "v_cache", true},
         {a->seq_lens, "seq_lens", true},
         {a->out, "out", true},
-        {a->v_scale, "v_scale", d->kv_dtype == UAA_DTYPE_VQ8 || d->kv_dtype == UAA_DTYPE_Q8},
-        {a->k_scale, "k_scale", d->kv_dtype == UAA_DTYPE_Q8},
+        {a->v_scale, "v_scale", scaled_values(d)},
+        {a->k_scale, "k_scale", scaled_keys(d)},
         {a->q_norm_w, "q_norm_w", need_io && d->qk_norm},
         {a->k_norm_w, "k_norm_w", need_io && d->qk_norm},
         {a->sink, "sink", d->has_sink != 0},
@@ -538,6 +575,23 @@ uaa_status run_partial(const uaa_attn_desc* d, const uaa_step_args* a, const uaa
         const CUtensorMapSwizzle code_sw = D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
         auto encode_set = [&](uint32_t box_rows, CUtensorMap& tk, CUtensorMap& tv, CUtensorMap& ts,
                               CUtensorMap& tks) -> uaa_status {
+            if (d->kv_dtype == UAA_DTYPE_Q4) {
+                // rows of D / 2 code bytes in one box each; a key's D / 32 fp16 scales as one
+                // element of 4 or 8 bytes (two of 8 at head_dim 256)
+                const CUtensorMapSwizzle sw = D == 64    ? CU_TENSOR_MAP_SWIZZLE_32B
+                                              : D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                         : CU_TENSOR_MAP_SWIZZLE_128B;
+                const CUtensorMapDataType st = D == 64 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT64;
+                const uint64_t per_key = D == 256 ? 2 : 1, row = scale_inner * (D / 16);
+                UAA_TRY(encode_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->k_cache, D / 2, rows, D / 2, (uint32_t)D / 2,
+                                  box_rows, sw, "k_cache 4-bit codes"));
+                UAA_TRY(encode_2d(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->v_cache, D / 2, rows, D / 2, (uint32_t)D / 2,
+                                  box_rows, sw, "v_cache 4-bit codes"));
+                UAA_TRY(encode_2d(&tks, st, a->k_scale, scale_inner * per_key, heads, row, box_rows * (uint32_t)per_key,
+                                  1, CU_TENSOR_MAP_SWIZZLE_NONE, "k_scale"));
+                return encode_2d(&ts, st, a->v_scale, scale_inner * per_key, heads, row, box_rows * (uint32_t)per_key, 1,
+                                 CU_TENSOR_MAP_SWIZZLE_NONE, "v_scale");
+            }
             if (d->kv_dtype == UAA_DTYPE_Q8) {
                 UAA_TRY(encode_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->k_cache, D, rows, D, code_box, box_rows,
                                   code_sw, "k_cache codes"));
@@ -890,6 +944,54 @@ uaa_status uaa_vq8_quantize(const void* v, int32_t v_dtype, int64_t n_rows, int3
         return fail(UAA_ERR_INVALID_ARGUMENT, "vq8_quantize pointers must be 16-byte aligned");
     const cudaError_t e = uaa::launch_vq8_quantize(v, v_dtype, n_rows, head_dim, codes, scales, stream);
     return e == cudaSuccess ? UAA_OK : cuda_fail(e, "vq8 quantize kernel launch");
+}
+
+uaa_status uaa_q4_quantize(const void* x, int32_t x_dtype, int64_t n_rows, int32_t head_dim, uint8_t* codes,
+                           void* scales, cudaStream_t stream)
+{
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+        return fail(UAA_ERR_UNSUPPORTED, "head_dim=%d is not supported (supported: {64, 128, 256})", head_dim);
+    if (x_dtype != UAA_DTYPE_F32 && x_dtype != UAA_DTYPE_BF16)
+        return fail(UAA_ERR_UNSUPPORTED, "x_dtype=%d is not F32 or BF16", x_dtype);
+    if (n_rows < 0) return fail(UAA_ERR_INVALID_ARGUMENT, "n_rows=%lld is negative", (long long)n_rows);
+    if (n_rows > (1LL << 55)) return fail(UAA_ERR_UNSUPPORTED, "n_rows=%lld is above 2^55", (long long)n_rows);
+    if (n_rows == 0) return UAA_OK;
+    if (!x || !codes || !scales) return fail(UAA_ERR_INVALID_ARGUMENT, "a q4_quantize pointer is NULL");
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales))
+        return fail(UAA_ERR_INVALID_ARGUMENT, "q4_quantize pointers must be 16-byte aligned");
+    const cudaError_t e =
+        uaa::launch_q4_quantize(x, x_dtype, n_rows, head_dim, codes, static_cast<__half*>(scales), stream);
+    return e == cudaSuccess ? UAA_OK : cuda_fail(e, "q4 quantize kernel launch");
+}
+
+uaa_status uaa_cache_read(const uaa_attn_desc* desc, const uaa_step_args* args, const int32_t* start, int32_t n_rows,
+                          void* k_out, void* v_out, cudaStream_t stream)
+{
+    UAA_TRY(check_desc(desc));
+    UAA_TRY(check_cache(desc, args));
+    if (n_rows < 0) return fail(UAA_ERR_INVALID_ARGUMENT, "n_rows=%d is negative", n_rows);
+    if (!aligned16(k_out) || !aligned16(v_out))
+        return fail(UAA_ERR_INVALID_ARGUMENT, "cache_read outputs must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(start) & 3u) return fail(UAA_ERR_INVALID_ARGUMENT, "start is not 4-byte aligned");
+    if (args->batch == 0 || n_rows == 0 || (!k_out && !v_out)) return UAA_OK;
+    uaa::ReadParams p{};
+    p.B = args->batch;
+    p.Hkv = desc->n_kv_heads;
+    p.D = desc->head_dim;
+    p.cap = args->cache_capacity;
+    p.n = n_rows;
+    p.kv_dtype = desc->kv_dtype;
+    p.out_dtype = desc->out_dtype;
+    p.start = start;
+    p.k_cache = args->k_cache;
+    p.v_cache = args->v_cache;
+    p.k_scale = args->k_scale;
+    p.v_scale = args->v_scale;
+    p.pages = pages_of(args);
+    p.k_out = k_out;
+    p.v_out = v_out;
+    const cudaError_t e = uaa::launch_cache_read(p, stream);
+    return e == cudaSuccess ? UAA_OK : cuda_fail(e, "cache read kernel launch");
 }
 
 uaa_status uaa_device_status(const uaa_workspace* ws, cudaStream_t stream, uint32_t* flags)

@@ -182,7 +182,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 2) append_kernel(const Appe
             const size_t slot = static_cast<size_t>(crow) * D;
             if (!is_q && !is_k) {  // value row: stored as given (or quantised)
                 if (!stores) return;
-                if (p.kv_dtype == UAA_DTYPE_VQ8 || p.kv_dtype == UAA_DTYPE_Q8) {
+                if (p.kv_dtype == UAA_DTYPE_Q4) {
+                    q4_store_row<EPL>(x, lane, static_cast<uint8_t*>(p.v_cache) + slot / 2,
+                                      reinterpret_cast<__half*>(p.v_scale) + slot / 32);
+                } else if (p.kv_dtype == UAA_DTYPE_VQ8 || p.kv_dtype == UAA_DTYPE_Q8) {
                     quantize_row<EPL>(x, lane, static_cast<int8_t*>(p.v_cache) + slot, p.v_scale + crow);
                 } else {
 #pragma unroll
@@ -206,7 +209,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 2) append_kernel(const Appe
             __syncwarp();
 
             // keys of a bf16 (or vq8) cache: rounded as their exact values (bf16_near_boundary)
-            const bool kbf16 = is_k && stores && p.kv_dtype != UAA_DTYPE_F32 && p.kv_dtype != UAA_DTYPE_Q8;
+            const bool codes = p.kv_dtype == UAA_DTYPE_Q8 || p.kv_dtype == UAA_DTYPE_Q4;  // keys are quantised
+            const bool kbf16 = is_k && stores && p.kv_dtype != UAA_DTYPE_F32 && !codes;
             bool row_inv_done = false;
             double row_inv64 = 0.0;
             for (int pp = lane; pp < HALF; pp += 32) {
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 2) append_kernel(const Appe
                         p.q_rot_out[in_row + ia] = ya;
                         p.q_rot_out[in_row + ib] = yb;
                     }
-                } else if (stores && p.kv_dtype == UAA_DTYPE_Q8) {  // the whole rotated row first: its scale
+                } else if (stores && codes) {  // the whole rotated row first: its scale
                     rowbuf[warp][ia] = ya;                            // needs max |k| (pairs are disjoint)
                     rowbuf[warp][ib] = yb;
                 } else if (kbf16) {
@@ -267,11 +271,15 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 2) append_kernel(const Appe
                 }
             }
             __syncwarp();
-            if (is_k && stores && p.kv_dtype == UAA_DTYPE_Q8) {  // q8 key: codes and scale of the rotated row
+            if (is_k && stores && codes) {  // q8, q4 key: codes and scales of the rotated row
                 float y[EPL];
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) y[i] = rowbuf[warp][lane + 32 * i];
-                quantize_row<EPL>(y, lane, static_cast<int8_t*>(p.k_cache) + slot, p.k_scale + crow);
+                if (p.kv_dtype == UAA_DTYPE_Q4)
+                    q4_store_row<EPL>(y, lane, static_cast<uint8_t*>(p.k_cache) + slot / 2,
+                                      reinterpret_cast<__half*>(p.k_scale) + slot / 32);
+                else
+                    quantize_row<EPL>(y, lane, static_cast<int8_t*>(p.k_cache) + slot, p.k_scale + crow);
                 __syncwarp();  // the row is read before the next one overwrites it
             }
     };
@@ -400,6 +408,15 @@ __device__ __forceinline__ void store8_codes(int8_t* dst, const float (&y)[8], f
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(vq8_code(y[i], s))) << (8 * (i & 3));
     *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+}
+
+// The 4-bit codes of 8 values with scale s.
+__device__ __forceinline__ uint32_t q4_word(const float (&y)[8], float s)
+{
+    uint32_t w = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w |= q4_nibble(y[i], s) << (4 * i);
+    return w;
 }
 
 // Sum / maximum over the U lanes that hold one head row (aligned groups of U lanes).
@@ -674,6 +691,25 @@ __global__ void __launch_bounds__(kStagedThreads, 2) append_staged_kernel(const 
             // row maximum for the int8 codes (q8 keys after the rotation, vq8 / q8 values)
             const bool quant = kind == 1 ? p.kv_dtype == UAA_DTYPE_Q8
                                          : kind == 2 && (p.kv_dtype == UAA_DTYPE_VQ8 || p.kv_dtype == UAA_DTYPE_Q8);
+            // 4-bit groups of 32 dims: each run of 8 with those of the 4 neighbouring threads
+            // (NeoX halves), or both runs with those of the next thread
+            const bool q4 = kind > 0 && p.kv_dtype == UAA_DTYPE_Q4;
+            float g0 = 0.f, g1 = 0.f;
+            if (__any_sync(0xffffffffu, valid && q4)) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    g0 = fmaxf(g0, fabsf(x0[j]));
+                    g1 = fmaxf(g1, fabsf(x1[j]));
+                }
+                if (!neox_rot) g0 = g1 = fmaxf(g0, g1);
+                g0 = fmaxf(g0, __shfl_xor_sync(0xffffffffu, g0, 1));
+                g1 = fmaxf(g1, __shfl_xor_sync(0xffffffffu, g1, 1));
+                const float h0 = __shfl_xor_sync(0xffffffffu, g0, 2), h1 = __shfl_xor_sync(0xffffffffu, g1, 2);
+                if (neox_rot) {
+                    g0 = fmaxf(g0, h0);
+                    g1 = fmaxf(g1, h1);
+                }
+            }
             float amax = 0.f;
             if (__any_sync(0xffffffffu, valid && quant)) {
 #pragma unroll
@@ -692,7 +728,15 @@ __global__ void __launch_bounds__(kStagedThreads, 2) append_staged_kernel(const 
                 }
             } else if (stores) {
                 const size_t slot = static_cast<size_t>(crow) * D;
-                if (quant) {
+                if (q4) {
+                    const __half s0 = q4_scale(g0), s1 = q4_scale(g1);
+                    uint8_t* codes = static_cast<uint8_t*>(kind == 1 ? p.k_cache : p.v_cache) + slot / 2;
+                    __half* sc = reinterpret_cast<__half*>(kind == 1 ? p.k_scale : p.v_scale) + slot / 32;
+                    *reinterpret_cast<uint32_t*>(codes + e0 / 2) = q4_word(x0, __half2float(s0));
+                    *reinterpret_cast<uint32_t*>(codes + e1 / 2) = q4_word(x1, __half2float(s1));
+                    if (e0 % 32 == 0) sc[e0 / 32] = s0;
+                    if (e1 % 32 == 0) sc[e1 / 32] = s1;
+                } else if (quant) {
                     const float s = vq8_scale(amax);
                     int8_t* codes = static_cast<int8_t*>(kind == 1 ? p.k_cache : p.v_cache) + slot;
                     store8_codes(codes + e0, x0, s);
@@ -715,7 +759,7 @@ __global__ void __launch_bounds__(kStagedThreads, 2) append_staged_kernel(const 
             // recomputed from the staged row) reaches one; an unrotated, unnormalised
             // element is exact.
             unsigned near = 0;
-            if (stores && kind == 1 && p.kv_dtype != UAA_DTYPE_F32 && p.kv_dtype != UAA_DTYPE_Q8) {
+            if (stores && kind == 1 && p.kv_dtype != UAA_DTYPE_F32 && p.kv_dtype != UAA_DTYPE_Q8 && !q4) {
                 float a0[8], a1[8];
                 load8<T>(row, e0, a0);
                 load8<T>(row, e1, a1);
@@ -859,6 +903,8 @@ bool launch_staged(const AppendParams& p, cudaStream_t s, cudaError_t& err)
 {
     auto a16 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
     if (p.q_len < 2 || (p.style == UAA_ROPE_NEOX && p.half_rot % 8 != 0)) return false;
+    // a 4-bit group of 32 dims is 8 elements of 4 threads (NeoX halves) or 16 of 2
+    if (p.kv_dtype == UAA_DTYPE_Q4 && p.style == UAA_ROPE_NEOX && p.half_rot % 32 != 0) return false;
     if (!a16(p.q) || !a16(p.k_new) || !a16(p.v_new) || !a16(p.k_cache) || !a16(p.v_cache) || !a16(p.q_prime) ||
         !a16(p.q_rot_out))
         return false;

@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -261,6 +262,26 @@ cudaError_t launch_prefill_umma(const PrefillParams& p, const CUtensorMap& tk, c
 constexpr int kPrefillRows = 128;
 constexpr int kPrefillKeys = 128;
 cudaError_t launch_step_f32(const StepF32Params& p, cudaStream_t s);
+// The same for 4-bit caches (partial_q4.cu; launch_partial_tc calls it).
+cudaError_t launch_partial_q4(const PartialParams& p, const PartialMaps& m, int n_head_tiles, int n_ctas, cudaStream_t s);
+cudaError_t launch_q4_quantize(const void* x, int dtype, int64_t n_rows, int D, uint8_t* codes, __half* scales,
+                               cudaStream_t s);
+
+// Rows of a cache as values (cache_rows.cu).
+struct ReadParams {
+    int B, Hkv, D, cap;
+    int n;                  // rows per sequence
+    int kv_dtype, out_dtype;
+    const int* start;       // [B] first position per sequence, or null (0)
+    const void* k_cache;
+    const void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    KvPages pages;
+    void* k_out;            // [B][n][Hkv][D], or null
+    void* v_out;
+};
+cudaError_t launch_cache_read(const ReadParams& p, cudaStream_t s);
 cudaError_t launch_vq8_quantize(const void* v, int v_dtype, int64_t n_rows, int D, int8_t* codes,
                                 float* scales, cudaStream_t s);
 
@@ -712,6 +733,42 @@ __device__ __forceinline__ int8_t vq8_code(float v, float s)
     if (s == 0.f) return 0;
     const float c = fminf(fmaxf(rintf(__fdiv_rn(v, s)), -127.f), 127.f);
     return static_cast<int8_t>(static_cast<int>(c));
+}
+
+// 4-bit storage rule of a group of 32 dims with max|x| = amax: the scale s = amax / 7
+// (IEEE division) rounded to bf16, at most 2720, held as fp16 (8 significant bits;
+// fewer where fp16 is subnormal), codes rint(x / s) (ties to even) within [-7, 7]
+// stored as nibbles code + 8, dim 2 i in the low nibble of byte i; s = 0 gives codes
+// 0. Eight significant bits so that code * s (11 bits) and 24 * s (10 bits) are fp16
+// numbers: the attention widens codes to their exact values in one fused
+// multiply-add. Against a scale of 11 bits the step is wider by 2^-9 at most.
+// Values beyond 7 * 2720 saturate.
+constexpr float kQ4MaxScale = 2720.f;
+
+__device__ __forceinline__ __half q4_scale(float amax)
+{
+    const float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(amax, 7.0f)));
+    return __float2half_rn(fminf(s, kQ4MaxScale));
+}
+
+__device__ __forceinline__ unsigned q4_nibble(float x, float s)
+{
+    if (s == 0.f) return 8u;
+    return static_cast<unsigned>(static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(x, s)), -7.f), 7.f)) + 8);
+}
+
+// Codes and scales of a row held EPL values per lane (dim lane + 32 i: group i).
+template <int EPL>
+__device__ __forceinline__ void q4_store_row(const float (&x)[EPL], int lane, uint8_t* codes, __half* scales)
+{
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const __half s = q4_scale(warp_max(fabsf(x[i])));
+        const unsigned u = q4_nibble(x[i], __half2float(s));
+        const unsigned hi = __shfl_down_sync(0xffffffffu, u, 1);
+        if (!(lane & 1)) codes[16 * i + (lane >> 1)] = static_cast<uint8_t>(u | hi << 4);
+        if (lane == 0) scales[i] = s;
+    }
 }
 
 // ---------------------------------------------------------------- range slots

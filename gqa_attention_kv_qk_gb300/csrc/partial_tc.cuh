@@ -79,8 +79,9 @@ __host__ __device__ constexpr int cta_threads(int nht) { return (consumer_warps(
 __host__ __device__ constexpr int round_up(int x, int a) { return (x + a - 1) / a * a; }
 
 // Cache kinds of the kernel's KV template argument: bf16 keys and values; vq8
-// (bf16 keys, int8 value codes + per-key scale); q8 (int8 codes for both).
-constexpr int kKvBf16 = 0, kKvVq8 = 1, kKvQ8 = 2;
+// (bf16 keys, int8 value codes + per-key scale); q8 (int8 codes for both); q4
+// (4-bit codes for both, a scale per key and 32 dims).
+constexpr int kKvBf16 = 0, kKvVq8 = 1, kKvQ8 = 2, kKvQ4 = 3;
 
 // MG: 16-key groups each consumer warp takes per stage: where a key costs few
 // bytes the consumers, not HBM, set the pace, and MG independent QK chains per
@@ -91,7 +92,7 @@ constexpr int kKvBf16 = 0, kKvVq8 = 1, kKvQ8 = 2;
 // three 128-key stages; 6-16 % faster than one group).
 template <int D, int KV, int NHT = 1>
 struct KeyGroups {
-    static constexpr int kMG = D == 64 ? (KV != kKvBf16 ? 4 : 2) : (KV == kKvQ8 || NHT == 2 ? 2 : 1);
+    static constexpr int kMG = D == 64 ? (KV != kKvBf16 ? 4 : 2) : (KV >= kKvQ8 || NHT == 2 ? 2 : 1);
 };
 
 // Shared memory, from a 1024-byte aligned base: the ring of kStages stages |
@@ -101,24 +102,30 @@ struct KeyGroups {
 template <int D, int KV, int NHT>
 struct Shape {
     static constexpr int kD = D;
-    static constexpr bool kVQ8 = KV != kKvBf16;              // int8 value codes + scales
+    static constexpr bool kVQ8 = KV == kKvVq8 || KV == kKvQ8;  // int8 value codes + scales
     static constexpr bool kKQ8 = KV == kKvQ8;                // int8 key codes + scales
+    static constexpr bool kQ4 = KV == kKvQ4;                 // 4-bit key and value codes + scales
+    static constexpr bool kVScaled = kVQ8 || kQ4, kKScaled = kKQ8 || kQ4;
     static constexpr int kMG = KeyGroups<D, KV, NHT>::kMG;
     static constexpr int kTK = kTileKeys * kMG;             // keys per stage
     static constexpr int kHC = 8 * NHT;                     // query heads of a unit
     static constexpr int kBoxBytes = kTK * 128;             // kTK rows x 128 bytes
     static constexpr int kCodeBoxes = D > 128 ? D / 128 : 1;  // boxes of an int8 code row
-    static constexpr int kKBoxes = kKQ8 ? kCodeBoxes : D / 64;
-    static constexpr int kVBoxes = kVQ8 ? kCodeBoxes : D / 64;
-    static constexpr int kKBytes = kKQ8 ? kTK * D : kTK * D * 2;
-    static constexpr int kVBytes = kVQ8 ? kTK * D : kTK * D * 2;
-    // bytes per row inside one box: 64 for int8 code rows at head_dim 64, else 128
-    static constexpr int kKRow = kKQ8 && D == 64 ? 64 : 128;
-    static constexpr int kVRow = kVQ8 && D == 64 ? 64 : 128;
-    // a stage: keys | values | value scales (int8 values) | key scales (int8 keys)
+    static constexpr int kKBoxes = kQ4 ? 1 : kKQ8 ? kCodeBoxes : D / 64;
+    static constexpr int kVBoxes = kQ4 ? 1 : kVQ8 ? kCodeBoxes : D / 64;
+    static constexpr int kKBytes = kQ4 ? kTK * D / 2 : kKQ8 ? kTK * D : kTK * D * 2;
+    static constexpr int kVBytes = kQ4 ? kTK * D / 2 : kVQ8 ? kTK * D : kTK * D * 2;
+    // bytes per row inside one box: D / 2 for 4-bit rows, 64 for int8 code rows at head_dim 64, else 128
+    static constexpr int kKRow = kQ4 ? D / 2 : kKQ8 && D == 64 ? 64 : 128;
+    static constexpr int kVRow = kQ4 ? D / 2 : kVQ8 && D == 64 ? 64 : 128;
+    // a stage: keys | values | value scales (int8 or 4-bit values) | key scales (int8
+    // or 4-bit keys); a key's scales are one fp32, or D / 32 fp16
+    static constexpr int kScaleRow = kQ4 ? D / 16 : 4;                // bytes of a key's scales
+    static constexpr int kScaleElems = kQ4 && D == 256 ? 2 : 1;       // and elements of the scales' tensor maps
     static constexpr int kVScaleOff = kKBytes + kVBytes;
-    static constexpr int kKScaleOff = kVScaleOff + (kVQ8 ? kTK * 4 : 0);
-    static constexpr int kSBytes = (kVQ8 ? kTK * 4 : 0) + (kKQ8 ? kTK * 4 : 0);
+    static constexpr int kKScaleOff = kVScaleOff + (kVScaled ? kTK * kScaleRow : 0);
+    static constexpr int kSBytes = ((kVScaled ? 1 : 0) + (kKScaled ? 1 : 0)) * kTK * kScaleRow;
+    static_assert(kScaleElems * kTK <= 256, "a TMA box has at most 256 elements a side");
     static constexpr int kStageBytes = round_up(kKBytes + kVBytes + kSBytes, 1024);
     static constexpr int kTxBytes = kKBytes + kVBytes + kSBytes;
     static constexpr int kPrefixBytes = round_up((kMaxSliceBatch + 1) * 4, 16);
@@ -129,7 +136,9 @@ struct Shape {
     static constexpr int kFragBytes = kHC * kFragRow;
     // a new key row (bf16, or int8 codes) at 0, value row (bf16, or int8 codes) at
     // 2 D, then for int8 values the value scale at 3 D and the key scale at 3 D + 4
-    static constexpr int kNewRowBytes = round_up(2 * D + (kVQ8 ? D + 8 : 2 * D), 16);
+    // q4: key codes at 0, value codes at D / 2, key scales at D, value scales at D + D / 16,
+    // then D floats that hold the rotated key row while its groups are quantised
+    static constexpr int kNewRowBytes = round_up(kQ4 ? 5 * D + D / 8 + 8 : 2 * D + (kVQ8 ? D + 8 : 2 * D), 16);
     // q-full and q-empty barriers, then the CTA's range slot, its weights, start, end, go flag
     static constexpr int kCtlBytes = 64;
     // fused append: theta'_p / pi (fp64) and the (cos, sin) of the current sequence, D / 2 each
@@ -156,11 +165,13 @@ __device__ __forceinline__ uint32_t tile_off(int row, int chunk)
     return static_cast<uint32_t>((chunk >> 3) * (TK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
 
-// The same for an int8 code stage of D-byte rows: D = 64 uses the 64-byte swizzle
-// (chunk XOR ((row / 2) mod 4)), D = 128 and 256 the 128-byte one per 128-byte box.
+// The same for a code stage of D-byte rows (int8 codes; 4-bit codes at half the
+// head_dim): D = 32 uses the 32-byte swizzle (chunk XOR ((row / 4) mod 2)), D = 64
+// the 64-byte one (chunk XOR ((row / 2) mod 4)), D = 128 and 256 the 128-byte one per 128-byte box.
 template <int D, int TK>
 __device__ __forceinline__ uint32_t code_off(int row, int chunk)
 {
+    if (D == 32) return static_cast<uint32_t>(row * 32 + ((chunk ^ ((row >> 2) & 1)) << 4));
     if (D == 64) return static_cast<uint32_t>(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
     return static_cast<uint32_t>((chunk >> 3) * (TK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
@@ -217,6 +228,33 @@ __device__ __forceinline__ void widen_code_quad(uint32_t r, uint32_t& d01, uint3
     d23 = hsub2_u32(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
 }
 
+// A register of 4-bit codes holds nibbles 0-3 of two 16-bit halves (values u =
+// code + 8). Returns the fp16 pair of nibble I of both halves as code * s, exactly:
+// u goes into mantissa bits 6-9 of 16 (fp16 0x4C00: 16 + u), and (16 + u) s - 24 s
+// is one fused multiply-add. s has at most 8 significant bits, so 24 s (10 bits)
+// and code * s (11 bits) are fp16 numbers. s: the two halves' scales, s24 = -24 s.
+template <int I>
+__device__ __forceinline__ uint32_t widen_q4(uint32_t r, uint32_t s, uint32_t s24)
+{
+    const uint32_t u = I == 0 ? r << 6 : I == 1 ? r << 2 : I == 2 ? r >> 2 : r >> 6;
+    uint32_t h = (u & 0x03C003C0u) | 0x4C004C00u;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(h) : "r"(h), "r"(s), "r"(s24));
+    return h;
+}
+
+__device__ __forceinline__ uint32_t neg24(uint32_t s)  // -24 s, both halves
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(0xCE00CE00u));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+
 __device__ __forceinline__ bool key_ok(int k, int lo, int hi) { return k >= lo && k < hi; }
 
 // Once per CTA the prep warp, having issued the reads of its first q rows, lets
@@ -230,6 +268,22 @@ __device__ __forceinline__ void release_producer(uint32_t go, int lane)
     if (lane == 0) ptx::flag_set(go, 1u);  // no __syncwarp: it too would wait for the reads
 }
 
+// N 32-bit words of shared memory, 4 N-byte aligned (N = 1, 2 or 4).
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* src, uint32_t (&w)[N])
+{
+    static_assert(N == 1 || N == 2 || N == 4, "one load");
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t*>(src);
+    } else if constexpr (N == 2) {
+        const uint2 a = *reinterpret_cast<const uint2*>(src);
+        w[0] = a.x, w[1] = a.y;
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4*>(src);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    }
+}
+
 // fp16 hi + lo parts of x into element e of a q' fragment row (the operands of
 // a q8 cache's int8 keys, which widen to fp16).
 __device__ __forceinline__ void store_frag_f16(uint8_t* row, int e, float x)
@@ -239,6 +293,21 @@ __device__ __forceinline__ void store_frag_f16(uint8_t* row, int e, float x)
     *reinterpret_cast<__half*>(row + (e >> 1) * 8 + (e & 1) * 2) = h;
     *reinterpret_cast<__half*>(row + (e >> 1) * 8 + 4 + (e & 1) * 2) = l;
 }
+
+// x as fp16 into a q' fragment row against 4-bit keys. A key register holds dims
+// 8t .. 8t + 7 of a 32-dim group (t = lane % 4) and widens to the pairs (i, i + 4):
+// the row keeps each 8 dims in the order 0 4 1 5 2 6 3 7, so a lane's operands of
+// two k-steps are 16 contiguous bytes. One fp16 part: rounding q' moves a logit by
+// 2^-12 of its terms (~1e-4 for logits of a few units), far below what 4-bit keys do.
+__device__ __forceinline__ void store_frag_q4(uint8_t* row, int e, float x)
+{
+    const int i = e & 7;
+    reinterpret_cast<__half*>(row)[(e & ~7) + 2 * (i & 3) + (i >> 2)] = __float2half_rn(x);
+}
+
+// How a q' row is held for the consumers: bf16 hi + lo parts (bf16 keys), fp16 hi +
+// lo parts (int8 keys), or one fp16 part (4-bit keys).
+constexpr int kFragBf16 = 0, kFragF16 = 1, kFragQ4 = 2;
 
 // bf16 hi + lo parts of x into element e of a q' fragment row.
 __device__ __forceinline__ void store_frag(uint8_t* row, int e, float x)
@@ -258,8 +327,8 @@ __device__ __forceinline__ void store_frag(uint8_t* row, int e, float x)
 // fragment rows (element e as fp32 at byte 4 e, the bytes its hi / lo pair
 // takes later) and each head is then finished in a rolled loop: at a launch's
 // start this code runs cold, and an unrolled body cost microseconds of
-// instruction fetch. F16: fp16 hi / lo parts (for int8 keys), else bf16.
-template <int D, int HC, typename T, bool F16>
+// instruction fetch.
+template <int D, int HC, typename T, int FRAG>
 __device__ void prep_fused_q(const PartialParams& p, int b, int h0, int nh, bool write_rot, bool new_seq, int pos,
                              const double* freq, float2* cs, uint8_t* frag, int row_bytes, uint32_t go, int lane)
 {
@@ -330,7 +399,10 @@ __device__ void prep_fused_q(const PartialParams& p, int b, int h0, int nh, bool
                     p.q_rot_out[qoff + ia[j]] = ya[j];
                     p.q_rot_out[qoff + ib[j]] = yb[j];
                 }
-                if (F16) {
+                if (FRAG == kFragQ4) {
+                    store_frag_q4(row, ia[j], ya[j] * p.qscale);
+                    store_frag_q4(row, ib[j], yb[j] * p.qscale);
+                } else if (FRAG == kFragF16) {
                     store_frag_f16(row, ia[j], ya[j] * p.qscale);
                     store_frag_f16(row, ib[j], yb[j] * p.qscale);
                 } else {
@@ -343,9 +415,8 @@ __device__ void prep_fused_q(const PartialParams& p, int b, int h0, int nh, bool
 }
 
 // Prep warp, separate append: the workspace's q' rows (already rotated and
-// prescaled, fp32) into the fragment slot, eight rows' loads at a time (fp16
-// parts for int8 keys when F16).
-template <int D, int HC, bool F16>
+// prescaled, fp32) into the fragment slot, eight rows' loads at a time.
+template <int D, int HC, int FRAG>
 __device__ __forceinline__ void prep_loaded_q(const PartialParams& p, int b, int kvh, int r0, int nh, uint8_t* frag,
                                               int row_bytes, uint32_t go, int lane)
 {
@@ -366,8 +437,13 @@ __device__ __forceinline__ void prep_loaded_q(const PartialParams& p, int b, int
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int j = 0; j < D / 64; ++j) {
+                if (FRAG == kFragQ4) {
+                    store_frag_q4(frag + (hc0 + i) * row_bytes, 2 * lane + 64 * j, x[i][j].x);
+                    store_frag_q4(frag + (hc0 + i) * row_bytes, 2 * lane + 64 * j + 1, x[i][j].y);
+                    continue;
+                }
                 uint32_t h, l;
-                if (F16)
+                if (FRAG == kFragF16)
                     split_f16(x[i][j].x, x[i][j].y, h, l);
                 else
                     split_bf16(x[i][j].x, x[i][j].y, h, l);
@@ -458,7 +534,7 @@ template <int D, int KV, typename T>
 __device__ void prep_new_rows(const PartialParams& p, int b, int kvh, int L, const float2* cs, uint8_t* staging,
                               bool store, int lane, NearQueue* nearq)
 {
-    constexpr bool VQ8 = KV != kKvBf16, KQ8 = KV == kKvQ8;
+    constexpr bool VQ8 = KV == kKvVq8 || KV == kKvQ8, KQ8 = KV == kKvQ8, Q4 = KV == kKvQ4;
     constexpr int NP = D / 64;   // rotation pairs per lane
     constexpr int EPL = D / 32;  // values per lane
     const size_t src = (static_cast<size_t>(b) * p.Hkv + kvh) * D;
@@ -496,6 +572,31 @@ __device__ void prep_new_rows(const PartialParams& p, int b, int kvh, int L, con
         ka0[j] = ka[j];
         kb0[j] = kb[j];
         rope_rotate(ka[j], kb[j], cs[lane + 32 * j]);
+    }
+    if (Q4) {  // the rotated row back in dim order (lane + 32 i is group i), then codes and scales of both rows
+        float* y = reinterpret_cast<float*>(staging + D + D / 8 + 8);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            y[ia[j]] = ka[j];
+            y[ib[j]] = kb[j];
+        }
+        __syncwarp();
+        float k[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) k[i] = y[lane + 32 * i];
+        __half* scales = reinterpret_cast<__half*>(staging + D);
+        q4_store_row<EPL>(k, lane, staging, scales);
+        q4_store_row<EPL>(v, lane, staging + D / 2, scales + D / 32);
+        __syncwarp();
+        if (store && lane < D / 16) {  // 16-byte chunks of codes, and their scales: keys, then values
+            const int c = lane % (D / 32);
+            const bool is_k = lane < D / 32;
+            const uint2 w0 = reinterpret_cast<const uint2*>(staging)[2 * lane], w1 = reinterpret_cast<const uint2*>(staging)[2 * lane + 1];
+            reinterpret_cast<uint4*>(static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) + slot * (D / 2))[c] =
+                make_uint4(w0.x, w0.y, w1.x, w1.y);
+            reinterpret_cast<__half*>(is_k ? p.k_scale : p.v_scale)[slot * (D / 32) + c] = scales[lane];
+        }
+        return;
     }
     if (KQ8) {  // the rotated row's codes, by the vq8 rule over the whole row
         float amax = 0.f;
@@ -633,12 +734,14 @@ __device__ __forceinline__ void issue_rows(uint32_t st, int r0, const CUtensorMa
 #pragma unroll
     for (int c = 0; c < SH::kKBoxes; ++c)
         ptx::tma_load_2d_hint(st + c * SH::kBoxBytes + r0 * SH::kKRow, tk, c * (SH::kKQ8 ? 128 : 64), y, bar, policy);
-    if (SH::kKQ8) ptx::tma_load_2d_hint(st + SH::kKScaleOff + 4 * r0, tks, sx, sy, bar, policy);
+    if (SH::kKScaled)
+        ptx::tma_load_2d_hint(st + SH::kKScaleOff + SH::kScaleRow * r0, tks, SH::kScaleElems * sx, sy, bar, policy);
 #pragma unroll
     for (int c = 0; c < SH::kVBoxes; ++c)
         ptx::tma_load_2d_hint(st + SH::kKBytes + c * SH::kBoxBytes + r0 * SH::kVRow, tv, c * (SH::kVQ8 ? 128 : 64),
                               y, bar, policy);
-    if (SH::kVQ8) ptx::tma_load_2d_hint(st + SH::kVScaleOff + 4 * r0, ts, sx, sy, bar, policy);
+    if (SH::kVScaled)
+        ptx::tma_load_2d_hint(st + SH::kVScaleOff + SH::kScaleRow * r0, ts, SH::kScaleElems * sx, sy, bar, policy);
 }
 
 // Owner warp of the new key: the staged rows over row r of the loaded stage.
@@ -647,6 +750,19 @@ __device__ __forceinline__ void patch_stage_row(const uint8_t* staging, uint8_t*
 {
     constexpr int D = SH::kD;
     constexpr int TK = SH::kTK;
+    if (SH::kQ4) {
+        constexpr int NC = D / 32;  // 16-byte chunks of a row of codes
+        if (lane < 2 * NC) {        // key codes by lanes 0 .. NC - 1, value codes by the next NC
+            const int c = lane % NC;
+            uint8_t* to = stage + (lane < NC ? 0 : SH::kKBytes) + code_off<D / 2, TK>(r, c);
+            *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(staging + 16 * lane);
+            *reinterpret_cast<uint2*>(to + 8) = *reinterpret_cast<const uint2*>(staging + 16 * lane + 8);
+            reinterpret_cast<__half*>(stage + (lane < NC ? SH::kKScaleOff : SH::kVScaleOff) + SH::kScaleRow * r)[c] =
+                reinterpret_cast<const __half*>(staging + D)[lane];
+        }
+        __syncwarp();
+        return;
+    }
     if (SH::kKQ8) {
         for (int c = lane; c < D / 16; c += 32)
             *reinterpret_cast<uint4*>(stage + code_off<D, TK>(r, c)) = *reinterpret_cast<const uint4*>(staging + 16 * c);
@@ -684,6 +800,8 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     using SH = Shape<D, KV, NHT>;
     constexpr bool VQ8 = SH::kVQ8;  // int8 value codes
     constexpr bool KQ8 = SH::kKQ8;  // int8 key codes
+    constexpr bool Q4 = SH::kQ4;    // 4-bit key and value codes
+    constexpr int FRAG = Q4 ? kFragQ4 : KQ8 ? kFragF16 : kFragBf16;
     constexpr int MG = SH::kMG;     // 16-key groups per warp per stage
     constexpr int TK = SH::kTK;     // keys per stage
     constexpr int KS = D / 16;      // k-steps of QK, m-tiles of PV
@@ -736,13 +854,13 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     } else if (threadIdx.x == 32 * kProducerWarp) {
         ptx::prefetch_tensormap(&tm_k);
         ptx::prefetch_tensormap(&tm_v);
-        if (VQ8) ptx::prefetch_tensormap(&tm_s);
-        if (KQ8) ptx::prefetch_tensormap(&tm_ks);
+        if (SH::kVScaled) ptx::prefetch_tensormap(&tm_s);
+        if (SH::kKScaled) ptx::prefetch_tensormap(&tm_ks);
         if (MG > 1 && !p.pages.table) {  // the 64-key maps of units' partial last stages
             ptx::prefetch_tensormap(&tm_kt);
             ptx::prefetch_tensormap(&tm_vt);
-            if (VQ8) ptx::prefetch_tensormap(&tm_st);
-            if (KQ8) ptx::prefetch_tensormap(&tm_kst);
+            if (SH::kVScaled) ptx::prefetch_tensormap(&tm_st);
+            if (SH::kKScaled) ptx::prefetch_tensormap(&tm_kst);
         }
     }
     grid_dependency_wait();  // the step's inputs (and a separate append's rows) are complete
@@ -904,10 +1022,10 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 const bool rot = p.q_rot_out != nullptr && sg.st0 == 0;
                 uint8_t* st_row = staging + (seg & 1) * SH::kNewRowBytes;
                 if (p.io_dtype == UAA_DTYPE_F32)
-                    prep_fused_q<D, HC, float, KQ8>(p, sg.b, h0, nh, rot, sg.b != cs_b, fits ? L : 0, freq_s, cs_s,
+                    prep_fused_q<D, HC, float, FRAG>(p, sg.b, h0, nh, rot, sg.b != cs_b, fits ? L : 0, freq_s, cs_s,
                                                     frag, SH::kFragRow, seg == 0 ? go : 0u, lane);
                 else
-                    prep_fused_q<D, HC, __nv_bfloat16, KQ8>(p, sg.b, h0, nh, rot, sg.b != cs_b, fits ? L : 0, freq_s,
+                    prep_fused_q<D, HC, __nv_bfloat16, FRAG>(p, sg.b, h0, nh, rot, sg.b != cs_b, fits ? L : 0, freq_s,
                                                             cs_s, frag, SH::kFragRow, seg == 0 ? go : 0u, lane);
                 cs_b = sg.b;
                 // the q' fragments go to the consumers first; the new rows are needed only at
@@ -928,7 +1046,7 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 pos += sg.n_st;
                 continue;
             } else {
-                prep_loaded_q<D, HC, KQ8>(p, sg.b, sg.kvh, r0, nh, frag, SH::kFragRow, seg == 0 ? go : 0u, lane);
+                prep_loaded_q<D, HC, FRAG>(p, sg.b, sg.kvh, r0, nh, frag, SH::kFragRow, seg == 0 ? go : 0u, lane);
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar_qfull);
@@ -936,7 +1054,7 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         // the deferred key pairs, off the consumers' path: recomputed in fp64 and
         // written over the cache's fp32 rounding
-        if (p.fused && KV != kKvQ8) {
+        if (p.fused && KV < kKvQ8) {
             __syncwarp();
             if (p.io_dtype == UAA_DTYPE_F32)
                 fix_near_keys<D, float>(p, nearq, lane);
@@ -1001,7 +1119,11 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const uint8_t* row = frag + ((nt0 + nt) * 8 + g) * SH::kFragRow;
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
-                if (KQ8) {
+                if (Q4) {  // k-steps 2 c and 2 c + 1 of 32-dim group c: 16 bytes per lane
+                    const uint2 a = *reinterpret_cast<const uint2*>(row + (kk >> 1) * 64 + 16 * t + 8 * (kk & 1));
+                    qhi[nt][kk][0] = a.x;
+                    qhi[nt][kk][1] = a.y;
+                } else if (KQ8) {
                     const uint4 a = *reinterpret_cast<const uint4*>(row + (8 * kk + 2 * t) * 8);
                     qhi[nt][kk][0] = a.x;
                     qlo[nt][kk][0] = a.y;
@@ -1064,7 +1186,39 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                     for (int nt = 0; nt < NTW; ++nt)
                         sacc[mg][nt][0] = sacc[mg][nt][1] = sacc[mg][nt][2] = sacc[mg][nt][3] = 0.f;
-                if (KQ8) {
+                if (Q4) {
+                    // 4-bit keys: one ldmatrix.x4 covers 16 keys x 64 dims (groups 2 kc and 2 kc + 1);
+                    // register j holds key g (+8 for odd j), dims 8t .. 8t + 7 of group 2 kc + j / 2,
+                    // widened to code * scale in fp16, exactly; the pairs (i, i + 4) of the 8 dims
+                    // are the operands of two k-steps
+                    const uint8_t* ksc = base_ptr + s * SH::kStageBytes + SH::kKScaleOff;
+#pragma unroll
+                    for (int mg = 0; mg < MG; ++mg) {
+                        uint32_t sg2[D / 64], sg8[D / 64];  // the scales of keys g and g + 8, two groups a word
+                        load_words<D / 64>(ksc + (key_w + 16 * mg + g) * SH::kScaleRow, sg2);
+                        load_words<D / 64>(ksc + (key_w + 16 * mg + g + 8) * SH::kScaleRow, sg8);
+#pragma unroll
+                        for (int kc = 0; kc < D / 64; ++kc) {
+                            uint32_t r[4];
+                            ptx::ldsm_x4(r, st + code_off<D / 2, TK>(key_w + 16 * mg + lr + 8 * (lq & 1), 2 * kc + (lq >> 1)));
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const uint32_t s0 = __byte_perm(sg2[kc], 0, c ? 0x3232 : 0x1010), m0 = neg24(s0);
+                                const uint32_t s8 = __byte_perm(sg8[kc], 0, c ? 0x3232 : 0x1010), m8 = neg24(s8);
+                                const uint32_t a0[4] = {widen_q4<0>(r[2 * c], s0, m0), widen_q4<0>(r[2 * c + 1], s8, m8),
+                                                        widen_q4<1>(r[2 * c], s0, m0), widen_q4<1>(r[2 * c + 1], s8, m8)};
+                                const uint32_t a1[4] = {widen_q4<2>(r[2 * c], s0, m0), widen_q4<2>(r[2 * c + 1], s8, m8),
+                                                        widen_q4<3>(r[2 * c], s0, m0), widen_q4<3>(r[2 * c + 1], s8, m8)};
+                                const int kk = 2 * (2 * kc + c);
+#pragma unroll
+                                for (int nt = 0; nt < NTW; ++nt) {
+                                    ptx::mma_f16(sacc[mg][nt], a0, qhi[nt][kk][0], qhi[nt][kk][1]);
+                                    ptx::mma_f16(sacc[mg][nt], a1, qhi[nt][kk + 1][0], qhi[nt][kk + 1][1]);
+                                }
+                            }
+                        }
+                    }
+                } else if (KQ8) {
                     // int8 keys: one ldmatrix.x4 covers 16 keys x 32 dims (k-steps 2 kc and
                     // 2 kc + 1); register j holds key g (+8 for odd j), dims 4t .. 4t + 3 of
                     // 16-byte chunk 2 kc + j / 2, widened exactly to fp16 pairs
@@ -1213,7 +1367,10 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                     for (int nt = 0; nt < NTW; ++nt) {
                         uint32_t h01, l01, h23, l23;
-                        if (VQ8) {
+                        if (Q4) {  // one fp16 part: 2^-12 relative, on a weight of at most 1
+                            h01 = pack_f16(x[mg][nt][0], x[mg][nt][1]);
+                            h23 = pack_f16(x[mg][nt][2], x[mg][nt][3]);
+                        } else if (VQ8) {
                             split_f16(x[mg][nt][0] * w_g[mg], x[mg][nt][1] * w_g[mg], h01, l01);     // key g
                             split_f16(x[mg][nt][2] * w_g8[mg], x[mg][nt][3] * w_g8[mg], h23, l23);   // key g+8
                         } else {
@@ -1222,11 +1379,54 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         }
                         bph[nt][0] = ptx::movmatrix_trans(h01);
                         bph[nt][1] = ptx::movmatrix_trans(h23);
-                        bpl[nt][0] = ptx::movmatrix_trans(l01);
-                        bpl[nt][1] = ptx::movmatrix_trans(l23);
+                        if (!Q4) {
+                            bpl[nt][0] = ptx::movmatrix_trans(l01);
+                            bpl[nt][1] = ptx::movmatrix_trans(l23);
+                        }
                     }
                     const int krow = key_w + 16 * mg;  // this group's first row in the stage
-                    if (VQ8) {
+                    if (Q4) {
+                        // O^T += V^T . P^T from the 4-bit stage: ldmatrix.trans hands a lane the 4 dims
+                        // 32 c + 4 g .. + 3 (a b16 element) of keys 2t and 2t + 1; nibble i of both is the
+                        // fp16 pair of dim 4 g + i. m-tile 2 c has dims 4 g (row g) and 4 g + 1 (row
+                        // g + 8) of group c, m-tile 2 c + 1 dims 4 g + 2 and 4 g + 3.
+                        const uint32_t vst = st + SH::kKBytes;
+                        const uint8_t* vsc = base_ptr + s * SH::kStageBytes + SH::kVScaleOff;
+                        uint32_t w0[D / 64], w1[D / 64], w8[D / 64], w9[D / 64];  // scales of keys 2t, +1, +8, +9
+                        load_words<D / 64>(vsc + (krow + 2 * t) * SH::kScaleRow, w0);
+                        load_words<D / 64>(vsc + (krow + 2 * t + 1) * SH::kScaleRow, w1);
+                        load_words<D / 64>(vsc + (krow + 2 * t + 8) * SH::kScaleRow, w8);
+                        load_words<D / 64>(vsc + (krow + 2 * t + 9) * SH::kScaleRow, w9);
+                        if (!whole) {  // a masked key's scales may be anything: zero
+                            const int kq = kbase + 16 * mg + 2 * t;
+#pragma unroll
+                            for (int j = 0; j < D / 64; ++j) {
+                                if (!key_ok(kq, lo, hi)) w0[j] = 0u;
+                                if (!key_ok(kq + 1, lo, hi)) w1[j] = 0u;
+                                if (!key_ok(kq + 8, lo, hi)) w8[j] = 0u;
+                                if (!key_ok(kq + 9, lo, hi)) w9[j] = 0u;
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < D / 64; ++j) {
+                            uint32_t r[4];
+                            ptx::ldsm_x4_trans(r, vst + code_off<D / 2, TK>(krow + lr + 8 * (lq >> 1), 2 * j + (lq & 1)));
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const uint32_t s0 = __byte_perm(w0[j], w1[j], c ? 0x7632 : 0x5410), m0 = neg24(s0);
+                                const uint32_t s8 = __byte_perm(w8[j], w9[j], c ? 0x7632 : 0x5410), m8 = neg24(s8);
+                                const uint32_t a0[4] = {widen_q4<0>(r[c], s0, m0), widen_q4<1>(r[c], s0, m0),
+                                                        widen_q4<0>(r[2 + c], s8, m8), widen_q4<1>(r[2 + c], s8, m8)};
+                                const uint32_t a1[4] = {widen_q4<2>(r[c], s0, m0), widen_q4<3>(r[c], s0, m0),
+                                                        widen_q4<2>(r[2 + c], s8, m8), widen_q4<3>(r[2 + c], s8, m8)};
+#pragma unroll
+                                for (int nt = 0; nt < NTW; ++nt) {
+                                    ptx::mma_f16(o[nt][4 * j + 2 * c], a0, bph[nt][0], bph[nt][1]);
+                                    ptx::mma_f16(o[nt][4 * j + 2 * c + 1], a1, bph[nt][0], bph[nt][1]);
+                                }
+                            }
+                        }
+                    } else if (VQ8) {
                         // O^T += V^T . P^T straight from the int8 stage: one ldmatrix.x4.trans covers
                         // 16 keys x 32 values = m-tiles 2j (values 32j .. 32j+15) and 2j+1; in m-tile
                         // mi row g holds value 16 mi + 2g and row g + 8 holds 16 mi + 2g + 1.
@@ -1315,7 +1515,8 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int hc = (nt0 + nt) * 8 + 2 * t + (e & 1);
-                        const int d = VQ8 ? 16 * mi + 2 * g + (e >> 1) : 16 * mi + g + 8 * (e >> 1);
+                        const int d = Q4 ? 32 * (mi >> 1) + 4 * g + 2 * (mi & 1) + (e >> 1)
+                                    : VQ8 ? 16 * mi + 2 * g + (e >> 1) : 16 * mi + g + 8 * (e >> 1);
                         if (d >= c0 && d < c0 + RC) red_o[(kgrp * HC + hc) * (RC + 4) + d - c0] = o[nt][mi][e] * o_unit;
                     }
             ptx::named_barrier_sync(1, CW * 32);

@@ -26,10 +26,12 @@ class DecodeLayer:
     pages b P .. b P + P - 1) maps each sequence's logical pages to pool pages, of
     which there are n_pages (default: just enough). max_q_len: the most tokens per
     sequence one step takes (q, k_new, v_new of shape [B][T][H][D]); the
-    workspace is sized for it."""
+    workspace is sized for it. cache: the caller's own tensors for some of k_cache,
+    v_cache, k_scale, v_scale and seq_lens (a pool shared with other layers, a cache
+    filled before), used in place instead of new ones."""
 
     def __init__(self, cfg: dict, batch: int, capacity: int, device="cuda", page_size=None, block_table=None,
-                 n_pages=None, max_q_len=1):
+                 n_pages=None, max_q_len=1, cache=None):
         self.cfg = dict(cfg)
         self.device = _require_cuda(device)
         self.batch = int(batch)
@@ -53,20 +55,28 @@ class DecodeLayer:
             self.pages_per_seq = self.n_pages = 0
             self.block_table = None
             rows = (batch, Hkv, capacity)
-        kdt = torch.float32 if kv == "f32" else torch.bfloat16
-        if kv == "q8":
-            self.k_cache = torch.zeros((*rows, D), dtype=torch.int8, device=dev)
-            self.k_scale = torch.zeros(rows, dtype=torch.float32, device=dev)
-        else:
-            self.k_cache = torch.zeros((*rows, D), dtype=kdt, device=dev)
-            self.k_scale = None
-        if kv in ("vq8", "q8"):
-            self.v_cache = torch.zeros((*rows, D), dtype=torch.int8, device=dev)
-            self.v_scale = torch.zeros(rows, dtype=torch.float32, device=dev)
-        else:
-            self.v_cache = torch.zeros((*rows, D), dtype=kdt, device=dev)
-            self.v_scale = None
-        self.seq_lens = torch.zeros((batch,), dtype=torch.int32, device=dev)
+        cache = dict(cache or {})
+
+        def tensor(name, shape, dtype):
+            t = cache.pop(name, None)
+            if t is None:
+                return torch.zeros(shape, dtype=dtype, device=dev)
+            if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"cache[{name!r}] is {tuple(t.shape)} {t.dtype} on {t.device}, the layer needs a "
+                                 f"contiguous {tuple(shape)} {dtype} on its device")
+            return t
+
+        row_of = {"f32": (D, torch.float32), "bf16": (D, torch.bfloat16), "q8": (D, torch.int8),
+                  "q4": (D // 2, torch.uint8)}
+        for which in ("k", "v"):
+            kind = ("bf16" if which == "k" else "q8") if kv == "vq8" else kv
+            width, dt = row_of[kind]
+            setattr(self, which + "_cache", tensor(which + "_cache", (*rows, width), dt))
+            scale = {"q8": (rows, torch.float32), "q4": ((*rows, D // 32), torch.float16)}.get(kind)
+            setattr(self, which + "_scale", tensor(which + "_scale", *scale) if scale else None)
+        self.seq_lens = tensor("seq_lens", (batch,), torch.int32)
+        if any(t is not None for t in cache.values()):
+            raise ValueError(f"a {kv} layer has no cache tensor named {sorted(cache)}")
         self.max_len_hint = 0
         self.out = torch.empty((batch, Hq, D), dtype=_TORCH_DTYPE[cfg.get("out_dtype", "f32")], device=dev)
         self._outs = {1: self.out}  # per tokens-per-step count: [B][Hq][D], or [B][T][Hq][D]
@@ -95,8 +105,8 @@ class DecodeLayer:
                         block_table=W.block_table(cfg, P, n_pages), n_pages=n_pages, max_q_len=T)
         else:
             layer = cls(cfg, cfg["batch"], case["cap"], device, max_q_len=T)
-        k = case["k_values"] if cfg.get("kv_dtype") == "q8" else case["k_cache"]
-        v = case["v_values"] if cfg.get("kv_dtype") in ("vq8", "q8") else case["v_cache"]
+        k = case["k_values"] if cfg.get("kv_dtype") in ("q8", "q4") else case["k_cache"]
+        v = case["v_values"] if cfg.get("kv_dtype") in ("vq8", "q8", "q4") else case["v_cache"]
         layer.load_cache(k, v, case["lens"])
         layer.set_params(case["q_norm_w"], case["k_norm_w"], case["sink"])
         return layer
@@ -126,18 +136,18 @@ class DecodeLayer:
 
     def load_cache(self, k, v, lens):
         """Copy host caches (logical rows [B][Hkv][cap][D]) in. For a vq8 layer `v`
-        holds fp32 values, and for a q8 layer `k` too, quantised on the device by
-        uaa_vq8_quantize (the append's own rule)."""
+        holds fp32 values, and for a q8 or q4 layer `k` too, quantised on the device by
+        uaa_vq8_quantize or uaa_q4_quantize (the append's own rules)."""
         D = self.cfg["head_dim"]
         s = torch.cuda.current_stream(self.device)
 
         def put(vals, cache, scales):
             if scales is not None:  # codes and scales of the logical rows, then into place
                 vals = vals.to(device=self.device, dtype=torch.float32).contiguous()
-                codes = torch.empty(vals.shape, dtype=torch.int8, device=self.device)
-                sc = torch.empty(vals.shape[:-1], dtype=torch.float32, device=self.device)
-                B.uaa_vq8_quantize(vals.data_ptr(), B.DTYPE["f32"], vals.numel() // D, D, codes.data_ptr(),
-                                   sc.data_ptr(), s)
+                codes = torch.empty((*vals.shape[:-1], cache.shape[-1]), dtype=cache.dtype, device=self.device)
+                sc = torch.empty((*vals.shape[:-1], *scales.shape[3:]), dtype=scales.dtype, device=self.device)
+                quantize = B.uaa_q4_quantize if cache.dtype == torch.uint8 else B.uaa_vq8_quantize
+                quantize(vals.data_ptr(), B.DTYPE["f32"], vals.numel() // D, D, codes.data_ptr(), sc.data_ptr(), s)
                 pairs = ((codes, cache), (sc, scales))
             else:
                 pairs = ((vals, cache),)
@@ -220,6 +230,24 @@ class DecodeLayer:
         if advance_hint and max_seq_len is None:
             self.max_len_hint += T
         return want if out is None else out
+
+    def read_rows(self, start, n, stream=None):
+        """The cached keys and values of positions start[b] .. start[b] + n - 1 of every
+        sequence (start: int32 tensor [B] on the device, or None for 0), as
+        [B][n][Hkv][D] tensors in the layer's out dtype; any cache kind, paged or not.
+        Positions outside the cache, or on absent pages, read as zeros."""
+        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if start is not None and (tuple(start.shape) != (self.batch,) or start.dtype != torch.int32
+                                  or not start.is_cuda or not start.is_contiguous()):
+            raise ValueError("start is not a contiguous int32 tensor [batch] on the device")
+        shape = (self.batch, int(n), self.cfg["n_kv_heads"], self.cfg["head_dim"])
+        k = torch.empty(shape, dtype=self.out.dtype, device=self.device)
+        v = torch.empty_like(k)
+        a = self.__dict__.get("_read_args")
+        if a is None:
+            a = self._read_args = self._build_args(None, None, None, 0, None, None)
+        B.uaa_cache_read(self.desc, a, B.ptr(start), int(n), B.ptr(k), B.ptr(v), s)
+        return k, v
 
     def append(self, q, k_new, v_new, stream=None, q_rot=None):
         s = stream if stream is not None else torch.cuda.current_stream(self.device)

@@ -22,7 +22,7 @@
  *      log-sum-exp) per range it touches in the workspace.
  *   3. uaa_decode_attn_combine: log-sum-exp merge of those records, the sink
  *      logit added to the denominator, the remaining output rows written.
- *   uaa_decode_attn_append_partial runs 1 and 2 (for bf16, vq8 and q8 caches and
+ *   uaa_decode_attn_append_partial runs 1 and 2 (for bf16, vq8, q8 and q4 caches and
  *   one token per sequence in one kernel that forms q', k and v of the new
  *   token itself and attends the new key from shared memory); uaa_decode_attn
  *   runs 1-3 on one stream.
@@ -99,8 +99,18 @@ typedef enum {
  * per token and kv head) or Q8 (keys stored like VQ8 values: the rotated key row
  * as int8 codes + its own scale). Codes follow the rule of uaa_vq8_quantize.
  * With Q8 the key codes meet q' (the normed, rotated q times the logit
- * prescale) as fp16 tensor-core operands: |q'| must stay below 65504. */
-typedef enum { UAA_DTYPE_F32 = 0, UAA_DTYPE_BF16 = 1, UAA_DTYPE_VQ8 = 2, UAA_DTYPE_Q8 = 3 } uaa_dtype;
+ * prescale) as fp16 tensor-core operands: |q'| must stay below 65504.
+ * Q4: keys and values as 4-bit codes, each group of 32 dims with its own fp16 scale
+ * (the rule of uaa_q4_quantize): a row is D / 2 bytes of codes and D / 32 scales.
+ * k_cache / v_cache then hold the codes ([..][D / 2] bytes), and k_scale / v_scale
+ * address the scales ([..][D / 32] fp16, cast to float*). |q'| as with Q8. */
+typedef enum {
+    UAA_DTYPE_F32 = 0,
+    UAA_DTYPE_BF16 = 1,
+    UAA_DTYPE_VQ8 = 2,
+    UAA_DTYPE_Q8 = 3,
+    UAA_DTYPE_Q4 = 4
+} uaa_dtype;
 
 /* Device-side status flags (sticky, in the workspace; read by uaa_device_status). */
 #define UAA_DEVFLAG_CAPACITY 0x1u   /* seq_lens[b] >= cache_capacity: that sequence was not appended */
@@ -153,7 +163,7 @@ typedef struct {
     int32_t window;           /* 0: none; W > 0: keys j with pos - W < j <= pos (and first_tokens) */
     float softcap;            /* 0: none; c > 0: s -> c tanh(s / c), after the scale */
     int32_t has_sink;         /* 1: sink[h] joins the softmax denominator of head h */
-    int32_t kv_dtype;         /* UAA_DTYPE_F32, _BF16, _VQ8 or _Q8 */
+    int32_t kv_dtype;         /* UAA_DTYPE_F32, _BF16, _VQ8, _Q8 or _Q4 */
     int32_t io_dtype;         /* q, k_new, v_new: UAA_DTYPE_F32 or _BF16 */
     int32_t out_dtype;        /* out: UAA_DTYPE_F32 or _BF16 */
     int32_t rotary_dim;       /* rotated dims per head: 0 (all D), or even, 2 <= R <= D */
@@ -179,13 +189,13 @@ typedef struct {
     const float* sink;        /* [Hq], required when has_sink */
     void* k_cache;            /* [B][Hkv][cap][D] */
     void* v_cache;            /* [B][Hkv][cap][D] */
-    float* v_scale;           /* [B][Hkv][cap], VQ8 and Q8 */
+    float* v_scale;           /* [B][Hkv][cap], VQ8 and Q8 (Q4: fp16 [B][Hkv][cap][D / 32]) */
     int32_t cache_capacity;   /* cap: slots per (sequence, kv head), a multiple of 4 */
     int32_t* seq_lens;        /* [B]: tokens cached before the step; the append adds 1 */
     int32_t max_seq_len;      /* host bound on seq_lens[b] before the step (+1 must fit cap) */
     void* out;                /* [B][Hq][D] out_dtype */
     float* q_rot;             /* optional [B][Hq][D] fp32: the normed, rotated q rows */
-    float* k_scale;           /* [B][Hkv][cap], Q8 only: the key rows' scales */
+    float* k_scale;           /* [B][Hkv][cap], Q8 only: the key rows' scales (Q4: as v_scale) */
     /* Paged caches (a key and a value per head per position, in pages: llamay
      * "What is refused" on what a KV page holds). block_table NULL: the caches
      * are contiguous, [B][Hkv][cap][...]. Otherwise k_cache / v_cache are pools
@@ -195,7 +205,7 @@ typedef struct {
      * table is read, never written; pages may be shared between sequences for
      * reading (a step writes slot seq_lens[b] of its own page only). */
     const int32_t* block_table; /* [B][pages_per_seq] int32, or NULL */
-    int32_t page_size;        /* keys per page: a power of two in [16, 4096]; >= 32 for VQ8 / Q8 */
+    int32_t page_size;        /* keys per page: a power of two in [16, 4096]; >= 32 for VQ8 / Q8 / Q4 */
     int32_t pages_per_seq;    /* row length of block_table */
     int32_t n_pages;          /* pages in each pool */
     /* Tokens per sequence in this step, T (0 counts as 1: a decode step). With
@@ -226,8 +236,8 @@ typedef struct {
 /* Where each array lives in the workspace, and the split geometry. */
 typedef struct {
     int32_t n_ctas;           /* P: persistent CTAs of the partial step (stream-K ranges) */
-    int32_t stage_keys;       /* keys per ring stage: 64; 128 for q8 at head_dim 128 / 256;
-                                 at head_dim 64 128 (bf16), 256 (vq8, q8) */
+    int32_t stage_keys;       /* keys per ring stage: 64; 128 for q8 and q4 at head_dim 128 / 256;
+                                 at head_dim 64 128 (bf16), 256 (vq8, q8, q4) */
     int32_t heads_per_cta;    /* query rows (token, head) of one unit (sequence, kv head, row group) */
     int32_t kernel;           /* 0: fp32 CUDA-core partial, 1: TMA + tensor-core partial,
                                  2: query-tiled prefill on a contiguous cache (bf16 cache,
@@ -285,7 +295,7 @@ uaa_status uaa_decode_attn_partial(const uaa_attn_desc* desc, const uaa_step_arg
 uaa_status uaa_decode_attn_combine(const uaa_attn_desc* desc, const uaa_step_args* args,
                                    const uaa_workspace* ws, cudaStream_t stream);
 
-/* Steps 1 and 2 on one stream. For bf16, vq8 and q8 caches this is one kernel: each
+/* Steps 1 and 2 on one stream. For bf16, vq8, q8 and q4 caches this is one kernel: each
  * unit normalises and rotates its q rows in registers (the workspace's q rows
  * are not written), the warp that owns slot seq_lens[b] of a unit's last key
  * stage forms the new k and v rows and writes them over that slot of the
@@ -335,6 +345,26 @@ uaa_status uaa_get_workspace_layout(const uaa_attn_desc* desc, int32_t batch,
  * Used to fill a vq8 cache from existing values, and the keys of a q8 cache. */
 uaa_status uaa_vq8_quantize(const void* v, int32_t v_dtype, int64_t n_rows, int32_t head_dim,
                             int8_t* codes, float* scales, cudaStream_t stream);
+
+/* Quantise n_rows rows of head_dim values (fp32 or bf16, x_dtype) to the Q4 storage
+ * (the append's rule). For each group of 32 dims s = max|x| / 7, rounded to 8
+ * significant bits (bf16, then fp16) and at most 2720, and codes = rint(x / s)
+ * (ties to even) within [-7, 7]; a row's codes go to D / 2 bytes as nibbles
+ * code + 8, dim 2 i in the low nibble of byte i, its scales to D / 32 fp16
+ * (scales). A value is code * s, exact in fp16; values beyond 19040 saturate, and
+ * a NaN is stored as some finite value. Used to fill a Q4 cache. */
+uaa_status uaa_q4_quantize(const void* x, int32_t x_dtype, int64_t n_rows, int32_t head_dim,
+                           uint8_t* codes, void* scales, cudaStream_t stream);
+
+/* Reads cached rows back as values: positions start[b] .. start[b] + n_rows - 1 of
+ * every sequence (start NULL: from 0) into k_out and v_out, [B][n_rows][Hkv][D] in
+ * desc->out_dtype (either may be NULL). Any cache kind, contiguous or paged; of args
+ * it uses batch, the caches, their scales, cache_capacity and the paging. A position
+ * outside [0, cache_capacity), or on a page that is not in the table, reads as
+ * zeros. Keys come as they are cached, rotated. */
+uaa_status uaa_cache_read(const uaa_attn_desc* desc, const uaa_step_args* args,
+                          const int32_t* start, int32_t n_rows, void* k_out, void* v_out,
+                          cudaStream_t stream);
 
 /* Waits for the stream, reads the device flags (UAA_DEVFLAG_*) of the workspace
  * into *flags, clears them, and returns UAA_ERR_DEVICE if any was set. */
