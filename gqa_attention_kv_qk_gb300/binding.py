@@ -22,6 +22,7 @@ UAA_DEVFLAG_CAPACITY = 0x1
 UAA_DEVFLAG_LEN_HINT = 0x2
 UAA_DEVFLAG_TIMEOUT = 0x4
 UAA_DEVFLAG_PAGE = 0x8
+UAA_DEVFLAG_POOL = 0x10
 
 ROPE_STYLE = {"neox": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "llama3": 1, "yarn": 2, "linear": 3}
@@ -57,6 +58,12 @@ class UaaStepArgs(ctypes.Structure):
                 ("out", ctypes.c_void_p), ("q_rot", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("block_table", ctypes.c_void_p), ("page_size", ctypes.c_int32),
                 ("pages_per_seq", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("q_len", ctypes.c_int32)]
+
+
+class UaaPageArgs(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("page_size", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("page_refs", ctypes.c_void_p), ("moves", ctypes.c_void_p), ("counts", ctypes.c_void_p)]
 
 
 class UaaWorkspace(ctypes.Structure):
@@ -109,6 +116,14 @@ _SIGS = [
     ("uaa_cache_read", ctypes.c_int,
      [_P(UaaAttnDesc), _P(UaaStepArgs), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
       ctypes.c_void_p]),
+    ("uaa_pages_workspace_size", ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+    ("uaa_pages_fork", ctypes.c_int, [_P(UaaPageArgs), ctypes.c_void_p, _P(UaaWorkspace), ctypes.c_void_p]),
+    ("uaa_pages_trim", ctypes.c_int,
+     [_P(UaaPageArgs), ctypes.c_int32, ctypes.c_int32, _P(UaaWorkspace), ctypes.c_void_p]),
+    ("uaa_pages_reserve", ctypes.c_int, [_P(UaaPageArgs), ctypes.c_int32, _P(UaaWorkspace), ctypes.c_void_p]),
+    ("uaa_pages_compact", ctypes.c_int, [_P(UaaPageArgs), _P(UaaWorkspace), ctypes.c_void_p]),
+    ("uaa_pages_copy", ctypes.c_int,
+     [_P(UaaPageArgs), _P(ctypes.c_void_p), _P(ctypes.c_int64), ctypes.c_int32, _P(UaaWorkspace), ctypes.c_void_p]),
     ("uaa_device_status", ctypes.c_int, [_P(UaaWorkspace), ctypes.c_void_p, _P(ctypes.c_uint32)]),
     ("uaa_last_error", ctypes.c_char_p, []),
     ("uaa_status_string", ctypes.c_char_p, [ctypes.c_int]),
@@ -221,6 +236,36 @@ def uaa_cache_read(desc, args, start_ptr: int, n_rows: int, k_out_ptr: int, v_ou
                    check=True) -> int:
     return _check(lib().uaa_cache_read(ctypes.byref(desc), ctypes.byref(args), ctypes.c_void_p(start_ptr), n_rows,
                                        ctypes.c_void_p(k_out_ptr), ctypes.c_void_p(v_out_ptr), _stream(stream)),
+                  check)
+
+
+def uaa_pages_workspace_size(batch: int, pages_per_seq: int, n_pages: int) -> int:
+    return int(lib().uaa_pages_workspace_size(batch, pages_per_seq, n_pages))
+
+
+def uaa_pages_fork(args, parents_ptr: int, ws, stream=None, check=True) -> int:
+    return _check(lib().uaa_pages_fork(ctypes.byref(args), ctypes.c_void_p(parents_ptr), ctypes.byref(ws),
+                                       _stream(stream)), check)
+
+
+def uaa_pages_trim(args, window: int, first_tokens: int, ws, stream=None, check=True) -> int:
+    return _check(lib().uaa_pages_trim(ctypes.byref(args), window, first_tokens, ctypes.byref(ws),
+                                       _stream(stream)), check)
+
+
+def uaa_pages_reserve(args, q_len: int, ws, stream=None, check=True) -> int:
+    return _check(lib().uaa_pages_reserve(ctypes.byref(args), q_len, ctypes.byref(ws), _stream(stream)), check)
+
+
+def uaa_pages_compact(args, ws, stream=None, check=True) -> int:
+    return _check(lib().uaa_pages_compact(ctypes.byref(args), ctypes.byref(ws), _stream(stream)), check)
+
+
+def uaa_pages_copy(args, pools, page_bytes, ws, stream=None, check=True) -> int:
+    """pools: device addresses; page_bytes: bytes of a page in each."""
+    n = len(pools)
+    return _check(lib().uaa_pages_copy(ctypes.byref(args), (ctypes.c_void_p * n)(*pools),
+                                       (ctypes.c_int64 * n)(*page_bytes), n, ctypes.byref(ws), _stream(stream)),
                   check)
 
 

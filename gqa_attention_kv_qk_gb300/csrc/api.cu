@@ -826,6 +826,81 @@ uaa_status run_step(const uaa_attn_desc* d, const uaa_step_args* a, const uaa_wo
     return run_combine(d, a, ws, pl, s);
 }
 
+// ---------------------------------------------------------------- pages of a cache
+
+// Workspace of the page operators: status word | a copy of the table | of the
+// lengths | a list of free pages | per page: requests, the last of them, its map.
+struct PageLayout {
+    size_t table, lens, list, asked, last, map, total;
+};
+
+uaa_status page_layout(int batch, int per_seq, int n_pages, PageLayout* lay)
+{
+    if (batch < 0) return fail(UAA_ERR_INVALID_ARGUMENT, "batch=%d is negative", batch);
+    if (per_seq <= 0) return fail(UAA_ERR_INVALID_ARGUMENT, "pages_per_seq=%d is not positive", per_seq);
+    if (n_pages <= 0) return fail(UAA_ERR_INVALID_ARGUMENT, "n_pages=%d is not positive", n_pages);
+    if ((long long)batch * per_seq > (1LL << 30) || n_pages > (1 << 30))
+        return fail(UAA_ERR_UNSUPPORTED, "batch*pages_per_seq=%lld or n_pages=%d exceeds 2^30", (long long)batch * per_seq,
+                    n_pages);
+    const size_t entries = align256((size_t)batch * per_seq * 4), pages = align256((size_t)n_pages * 4);
+    lay->table = 256;
+    lay->lens = lay->table + entries;
+    lay->list = lay->lens + align256((size_t)batch * 4);
+    lay->asked = lay->list + entries;
+    lay->last = lay->asked + pages;
+    lay->map = lay->last + pages;
+    lay->total = lay->map + pages;
+    return UAA_OK;
+}
+
+uaa_status page_params(const uaa_page_args* a, const uaa_workspace* ws, uaa::PageParams* p)
+{
+    if (!a) return fail(UAA_ERR_INVALID_ARGUMENT, "args is NULL");
+    if (!ws || !ws->ptr) return fail(UAA_ERR_INVALID_ARGUMENT, "workspace is NULL");
+    if (!aligned16(ws->ptr)) return fail(UAA_ERR_INVALID_ARGUMENT, "workspace is not 16-byte aligned");
+    if (a->page_size < 16 || a->page_size > 4096 || (a->page_size & (a->page_size - 1)) != 0)
+        return fail(UAA_ERR_UNSUPPORTED, "page_size=%d is not a power of two in [16, 4096]", a->page_size);
+    PageLayout lay;
+    UAA_TRY(page_layout(a->batch, a->pages_per_seq, a->n_pages, &lay));
+    if ((long long)a->pages_per_seq * a->page_size > 2147483647LL)
+        return fail(UAA_ERR_UNSUPPORTED, "pages_per_seq=%d x page_size=%d exceeds 2^31 positions", a->pages_per_seq,
+                    a->page_size);
+    if (ws->bytes < lay.total)
+        return fail(UAA_ERR_INVALID_ARGUMENT, "workspace has %zu bytes, the page operators need %zu", ws->bytes,
+                    lay.total);
+    const struct {
+        const void* q;
+        const char* name;
+        bool needed;
+    } ptrs[] = {{a->block_table, "block_table", a->batch > 0},
+                {a->seq_lens, "seq_lens", a->batch > 0},
+                {a->page_refs, "page_refs", true},
+                {a->moves, "moves", true},
+                {a->counts, "counts", true}};
+    for (auto& e : ptrs) {
+        if (e.needed && !e.q) return fail(UAA_ERR_INVALID_ARGUMENT, "%s is NULL", e.name);
+        if (e.q && !aligned16(e.q)) return fail(UAA_ERR_INVALID_ARGUMENT, "%s is not 16-byte aligned", e.name);
+    }
+    char* w = static_cast<char*>(ws->ptr);
+    p->B = a->batch;
+    p->per_seq = a->pages_per_seq;
+    p->page_size = a->page_size;
+    p->n_pages = a->n_pages;
+    p->table = a->block_table;
+    p->seq_lens = a->seq_lens;
+    p->refs = a->page_refs;
+    p->moves = a->moves;
+    p->counts = a->counts;
+    p->status = reinterpret_cast<unsigned*>(w);
+    p->table_tmp = reinterpret_cast<int*>(w + lay.table);
+    p->lens_tmp = reinterpret_cast<int*>(w + lay.lens);
+    p->list = reinterpret_cast<int*>(w + lay.list);
+    p->asked = reinterpret_cast<int*>(w + lay.asked);
+    p->last = reinterpret_cast<int*>(w + lay.last);
+    p->map = reinterpret_cast<int*>(w + lay.map);
+    return UAA_OK;
+}
+
 }  // namespace
 
 // ---------------------------------------------------------------- exported C ABI
@@ -994,6 +1069,80 @@ uaa_status uaa_cache_read(const uaa_attn_desc* desc, const uaa_step_args* args, 
     return e == cudaSuccess ? UAA_OK : cuda_fail(e, "cache read kernel launch");
 }
 
+size_t uaa_pages_workspace_size(int32_t batch, int32_t pages_per_seq, int32_t n_pages)
+{
+    PageLayout lay;
+    return page_layout(batch, pages_per_seq, n_pages, &lay) == UAA_OK ? lay.total : 0;
+}
+
+uaa_status uaa_pages_fork(const uaa_page_args* args, const int32_t* parents, const uaa_workspace* ws,
+                          cudaStream_t stream)
+{
+    uaa::PageParams p;
+    UAA_TRY(page_params(args, ws, &p));
+    if (p.B == 0) return UAA_OK;
+    if (!parents) return fail(UAA_ERR_INVALID_ARGUMENT, "parents is NULL");
+    if (reinterpret_cast<uintptr_t>(parents) & 3u)
+        return fail(UAA_ERR_INVALID_ARGUMENT, "parents is not 4-byte aligned");
+    const cudaError_t e = uaa::launch_pages_fork(p, parents, stream);
+    return e == cudaSuccess ? UAA_OK : cuda_fail(e, "page fork kernel launch");
+}
+
+uaa_status uaa_pages_trim(const uaa_page_args* args, int32_t window, int32_t first_tokens, const uaa_workspace* ws,
+                          cudaStream_t stream)
+{
+    uaa::PageParams p;
+    UAA_TRY(page_params(args, ws, &p));
+    if (window <= 0) return fail(UAA_ERR_UNSUPPORTED, "window=%d is not positive", window);
+    if (first_tokens < 0) return fail(UAA_ERR_UNSUPPORTED, "first_tokens=%d is negative", first_tokens);
+    if (p.B == 0) return UAA_OK;
+    const cudaError_t e = uaa::launch_pages_trim(p, window, first_tokens, stream);
+    return e == cudaSuccess ? UAA_OK : cuda_fail(e, "page trim kernel launch");
+}
+
+uaa_status uaa_pages_reserve(const uaa_page_args* args, int32_t q_len, const uaa_workspace* ws, cudaStream_t stream)
+{
+    uaa::PageParams p;
+    UAA_TRY(page_params(args, ws, &p));
+    if (q_len < 1 || q_len > kMaxQLen) return fail(UAA_ERR_UNSUPPORTED, "q_len=%d is not in [1, %d]", q_len, kMaxQLen);
+    const cudaError_t e = uaa::launch_pages_reserve(p, q_len, stream);
+    return e == cudaSuccess ? UAA_OK : cuda_fail(e, "page reserve kernel launch");
+}
+
+uaa_status uaa_pages_compact(const uaa_page_args* args, const uaa_workspace* ws, cudaStream_t stream)
+{
+    uaa::PageParams p;
+    UAA_TRY(page_params(args, ws, &p));
+    const cudaError_t e = uaa::launch_pages_compact(p, stream);
+    return e == cudaSuccess ? UAA_OK : cuda_fail(e, "page compact kernel launch");
+}
+
+uaa_status uaa_pages_copy(const uaa_page_args* args, void* const* pools, const int64_t* page_bytes, int32_t n_pools,
+                          const uaa_workspace* ws, cudaStream_t stream)
+{
+    uaa::PageParams p;
+    UAA_TRY(page_params(args, ws, &p));
+    if (n_pools < 0 || n_pools > uaa::kMaxPools)
+        return fail(UAA_ERR_UNSUPPORTED, "n_pools=%d is not in [0, %d]", n_pools, uaa::kMaxPools);
+    if (n_pools == 0) return UAA_OK;
+    if (!pools || !page_bytes) return fail(UAA_ERR_INVALID_ARGUMENT, "pools or page_bytes is NULL");
+    uaa::PagePools pp{};
+    for (int k = 0; k < n_pools; ++k) {
+        if (!pools[k]) return fail(UAA_ERR_INVALID_ARGUMENT, "pools[%d] is NULL", k);
+        if (!aligned16(pools[k])) return fail(UAA_ERR_INVALID_ARGUMENT, "pools[%d] is not 16-byte aligned", k);
+        if (page_bytes[k] <= 0 || page_bytes[k] % 16 != 0 || page_bytes[k] > (1LL << 31))
+            return fail(UAA_ERR_UNSUPPORTED, "page_bytes[%d]=%lld is not a positive multiple of 16 up to 2^31", k,
+                        (long long)page_bytes[k]);
+        pp.base[k] = static_cast<char*>(pools[k]);
+        pp.bytes[k] = page_bytes[k];
+    }
+    pp.n = n_pools;
+    const int n_sm = device_sm_count();
+    if (n_sm <= 0) return fail(UAA_ERR_CUDA, "no CUDA device: the SM count query failed");
+    const cudaError_t e = uaa::launch_pages_copy(p, pp, n_sm, stream);
+    return e == cudaSuccess ? UAA_OK : cuda_fail(e, "page copy kernel launch");
+}
+
 uaa_status uaa_device_status(const uaa_workspace* ws, cudaStream_t stream, uint32_t* flags)
 {
     if (!ws || !ws->ptr || !flags) return fail(UAA_ERR_INVALID_ARGUMENT, "workspace or flags is NULL");
@@ -1005,9 +1154,10 @@ uaa_status uaa_device_status(const uaa_workspace* ws, cudaStream_t stream, uint3
     if (e != cudaSuccess) return cuda_fail(e, "reading the device status word");
     *flags = f;
     if (f)
-        return fail(UAA_ERR_DEVICE, "device flags 0x%x:%s%s%s", f, (f & UAA_DEVFLAG_CAPACITY) ? " capacity" : "",
+        return fail(UAA_ERR_DEVICE, "device flags 0x%x:%s%s%s%s%s", f, (f & UAA_DEVFLAG_CAPACITY) ? " capacity" : "",
                     (f & UAA_DEVFLAG_LEN_HINT) ? " max_seq_len-exceeded" : "",
-                    (f & UAA_DEVFLAG_TIMEOUT) ? " wait-timeout" : "");
+                    (f & UAA_DEVFLAG_TIMEOUT) ? " wait-timeout" : "", (f & UAA_DEVFLAG_PAGE) ? " page" : "",
+                    (f & UAA_DEVFLAG_POOL) ? " pool-exhausted" : "");
     return UAA_OK;
 }
 

@@ -282,6 +282,37 @@ struct ReadParams {
     void* v_out;
 };
 cudaError_t launch_cache_read(const ReadParams& p, cudaStream_t s);
+
+// The pages of a paged cache (pages.cu).
+struct PageParams {
+    int B, per_seq, page_size, n_pages;
+    int* table;     // [B][per_seq]
+    int* seq_lens;  // [B]
+    int* refs;      // [n_pages]
+    int* moves;     // [n_pages][2] (src, dst)
+    int* counts;    // [4] moves, held pages, pages asked for
+    // workspace
+    unsigned* status;
+    int* table_tmp;  // [B][per_seq]
+    int* lens_tmp;   // [B]
+    int* list;       // [B][per_seq] free pages
+    int* asked;      // [n_pages] requests per held page (zero between calls)
+    int* last;       // [n_pages] the last of them, its table index + 1 (zero between calls)
+    int* map;        // [n_pages] where a compacted page went (-1: free before)
+};
+constexpr int kMaxPools = 8;
+struct PagePools {
+    int n;
+    int pieces;                  // pieces of one page over all pools (set by the launch)
+    int pool_pieces[kMaxPools];
+    char* base[kMaxPools];
+    int64_t bytes[kMaxPools];    // bytes of a page
+};
+cudaError_t launch_pages_fork(const PageParams& p, const int* parents, cudaStream_t s);
+cudaError_t launch_pages_trim(const PageParams& p, int window, int first_tokens, cudaStream_t s);
+cudaError_t launch_pages_reserve(const PageParams& p, int q_len, cudaStream_t s);
+cudaError_t launch_pages_compact(const PageParams& p, cudaStream_t s);
+cudaError_t launch_pages_copy(const PageParams& p, const PagePools& pools, int n_sm, cudaStream_t s);
 cudaError_t launch_vq8_quantize(const void* v, int v_dtype, int64_t n_rows, int D, int8_t* codes,
                                 float* scales, cudaStream_t s);
 

@@ -120,6 +120,10 @@ typedef enum {
                                        invalid until the workspace is zeroed again */
 #define UAA_DEVFLAG_PAGE 0x8u       /* a block_table entry outside [0, n_pages): that row was
                                        neither written nor read (outputs of the sequence invalid) */
+                                    /* (page operators: a table entry that is neither a page nor -1, or
+                                       a parent or move outside its range, was left alone) */
+#define UAA_DEVFLAG_POOL 0x10u      /* uaa_pages_reserve: fewer free pages than were asked for; nothing
+                                       was given, and the step must wait until pages are freed */
 
 /* Rotary embedding of the first R = rotary_dim dims of each head row (R = D when
  * the descriptor's rotary_dim is 0; the other D - R dims pass unchanged: the
@@ -365,6 +369,70 @@ uaa_status uaa_q4_quantize(const void* x, int32_t x_dtype, int64_t n_rows, int32
 uaa_status uaa_cache_read(const uaa_attn_desc* desc, const uaa_step_args* args,
                           const int32_t* start, int32_t n_rows, void* k_out, void* v_out,
                           cudaStream_t stream);
+
+/* The pages of a paged cache: what a serving loop does to the block table between
+ * steps. One block table and one count per page serve every layer; only the copies
+ * are per layer. All arrays are device memory, int32, 16-byte aligned.
+ *
+ * page_refs[p] counts the table entries that name page p (and whatever the caller
+ * pins besides); 0 is a free page. An entry of -1 is absent. The operators keep the
+ * counts; a table set up by hand must start with them right. Results do not depend
+ * on the order in which the GPU runs things.
+ *
+ * A branching search: uaa_pages_fork with each row's parent, uaa_pages_reserve for
+ * the step's tokens, uaa_pages_copy for each layer's pools, then the step. A long
+ * stream under a window: uaa_pages_trim after the step; uaa_pages_compact and
+ * uaa_pages_copy when the pool is to shrink. */
+typedef struct {
+    int32_t batch;            /* rows of the table, >= 0 */
+    int32_t page_size;        /* positions per page, as in uaa_step_args */
+    int32_t pages_per_seq;    /* row length of the table */
+    int32_t n_pages;          /* pages in each pool */
+    int32_t* block_table;     /* [batch][pages_per_seq] */
+    int32_t* seq_lens;        /* [batch]: tokens cached */
+    int32_t* page_refs;       /* [n_pages] */
+    int32_t* moves;           /* [n_pages][2]: (src, dst) pages to copy, written by reserve and
+                                 compact (entries at and past counts[0] are left as they were) */
+    int32_t* counts;          /* [4]: moves; held pages (compact); pages asked for (reserve); - */
+} uaa_page_args;
+
+/* Workspace bytes of the page operators (zeroed once; not the step's workspace; one
+ * per table, not shared by calls that may overlap). uaa_device_status reads its
+ * flags. 0 on refused sizes. */
+size_t uaa_pages_workspace_size(int32_t batch, int32_t pages_per_seq, int32_t n_pages);
+
+/* Every row b of the table, and its length, becomes a copy of row parents[b] as it
+ * was before the call; parents[b] = b keeps a row, -1 ends it (no pages, length 0).
+ * Pages are shared, not copied: reserve copies the ones that a step will write. */
+uaa_status uaa_pages_fork(const uaa_page_args* args, const int32_t* parents,
+                          const uaa_workspace* ws, cudaStream_t stream);
+
+/* Frees the pages that no later token sees under a window with first tokens (the
+ * descriptor's): those past the first tokens and wholly before the window of the
+ * token at seq_lens[b]. Their entries become -1, which the steps allow. */
+uaa_status uaa_pages_trim(const uaa_page_args* args, int32_t window, int32_t first_tokens,
+                          const uaa_workspace* ws, cudaStream_t stream);
+
+/* Gives every sequence pages of its own for its next q_len tokens. Absent pages, in
+ * order of (sequence, position), take the free pages in ascending order. A page
+ * that others hold too is replaced, and where it holds rows before the new tokens
+ * joined to the moves; if all who hold it ask, the last of them keeps it. All
+ * requests are served or none (UAA_DEVFLAG_POOL; counts[2] says how many pages were
+ * asked for). A sequence without room for q_len tokens asks for nothing. */
+uaa_status uaa_pages_reserve(const uaa_page_args* args, int32_t q_len, const uaa_workspace* ws,
+                             cudaStream_t stream);
+
+/* Moves held pages to the front of the pool: with n of them (counts[1]), the i-th
+ * held page at or past n goes to the i-th free page before n. Table and counts are
+ * renamed; pages n .. n_pages - 1 are free afterwards. */
+uaa_status uaa_pages_compact(const uaa_page_args* args, const uaa_workspace* ws, cudaStream_t stream);
+
+/* Copies the pages of the last reserve or compact (counts[0] moves) in every given
+ * pool: pool k holds page p in bytes p * page_bytes[k] .. (a multiple of 16). Up to
+ * eight pools a call; call it for each layer. Moves set up by hand: no page may be
+ * the destination of two, or of one and the source of another. */
+uaa_status uaa_pages_copy(const uaa_page_args* args, void* const* pools, const int64_t* page_bytes,
+                          int32_t n_pools, const uaa_workspace* ws, cudaStream_t stream);
 
 /* Waits for the stream, reads the device flags (UAA_DEVFLAG_*) of the workspace
  * into *flags, clears them, and returns UAA_ERR_DEVICE if any was set. */
