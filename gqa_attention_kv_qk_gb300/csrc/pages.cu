@@ -63,6 +63,44 @@ __global__ void __launch_bounds__(kPageThreads) fork_scatter_kernel(const PagePa
     if (i < p.B) p.seq_lens[i] = p.lens_tmp[i];
 }
 
+// A table of up to kForkEntries entries in one launch: one CTA holds all new rows in
+// registers before it writes any (2.5 us for the two launches, 1.6 for this one).
+constexpr int kForkThreads = 1024, kForkPer = 8;
+constexpr int kForkEntries = kForkThreads * kForkPer;
+
+__global__ void __launch_bounds__(kForkThreads) fork_small_kernel(const PageParams p, const int* parents)
+{
+    grid_dependency_wait();
+    const int n = p.B * p.per_seq;
+    int now[kForkPer], len[kForkPer];
+#pragma unroll
+    for (int k = 0; k < kForkPer; ++k) {
+        const int i = k * kForkThreads + threadIdx.x;
+        if (i >= n) break;
+        const int b = i / p.per_seq, l = i - b * p.per_seq;
+        int par = parents[b];
+        if (par < -1 || par >= p.B) {
+            if (l == 0) atomicOr(p.status, UAA_DEVFLAG_PAGE);
+            par = b;
+        }
+        const int old = p.table[i];
+        now[k] = par < 0 ? -1 : p.table[par * p.per_seq + l];
+        len[k] = l == 0 ? (par < 0 ? 0 : p.seq_lens[par]) : -1;
+        if (par == b) continue;
+        check_entry(p, old);
+        if (is_page(p, old)) atomicSub(p.refs + old, 1);
+        if (is_page(p, now[k])) atomicAdd(p.refs + now[k], 1);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kForkPer; ++k) {
+        const int i = k * kForkThreads + threadIdx.x;
+        if (i >= n) break;
+        p.table[i] = now[k];
+        if (i % p.per_seq == 0) p.seq_lens[i / p.per_seq] = len[k];
+    }
+}
+
 // ---------------------------------------------------------------- trim
 // Pages whose positions no later token sees (behind the window of the token that
 // comes next, and past the first tokens) leave the table.
@@ -164,6 +202,71 @@ __device__ __forceinline__ bool stays(const PageParams& p, const Request& r)
 {
     const int n = __ldcg(p.refs + r.e);
     return n <= 1 || (n == __ldcg(p.asked + r.e) && __ldcg(p.last + r.e) == r.at + 1);
+}
+
+// Up to a request per thread (most steps): each is read once and kept in registers,
+// the first pages' counts are on their way meanwhile, and the free pages go through
+// shared memory: four dependent round trips to memory.
+__global__ void __launch_bounds__(kScanThreads) reserve_small_kernel(const PageParams p, int q_len)
+{
+    __shared__ int buf[33];
+    __shared__ int list[kScanThreads];
+    grid_dependency_wait();
+    const int tid = threadIdx.x;
+    const int per = (q_len - 1) / p.page_size + 2;  // logical pages that q_len positions can touch
+    int cnt[kScanPer];
+    load_refs(p, static_cast<int64_t>(tid) * kScanPer, cnt);
+    const Request r = request_of(p, tid, per, q_len);
+    if (!r.wanted && r.e != 0) check_entry(p, r.e);
+    const bool held = r.wanted && r.held;
+    if (held) {
+        atomicAdd(p.asked + r.e, 1);
+        atomicMax(p.last + r.e, r.at + 1);
+    }
+    __threadfence();
+    __syncthreads();
+    const bool take = r.wanted && !(held && stays(p, r));
+    const bool copy = take && held && static_cast<int64_t>(r.l) * p.page_size < r.L;
+    int both;  // takes, and copies in the upper half (at most 1,024 each)
+    const int rank2 = block_prefix((take ? 1 : 0) | (copy ? 1 << 16 : 0), buf, both);
+    const int takes = both & 0xffff, rank = rank2 & 0xffff, c = rank2 >> 16;
+    int found = 0;
+    for (int64_t i0 = 0; i0 < p.n_pages && found < takes; i0 += kScanThreads * kScanPer) {
+        if (i0) load_refs(p, i0 + static_cast<int64_t>(tid) * kScanPer, cnt);
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < kScanPer; ++k) n += cnt[k] == 0;
+        int total;
+        int at = found + block_prefix(n, buf, total);
+#pragma unroll
+        for (int k = 0; k < kScanPer; ++k)
+            if (cnt[k] == 0) {
+                if (at < takes) list[at] = static_cast<int>(i0) + tid * kScanPer + k;
+                ++at;
+            }
+        found += total;
+    }
+    __syncthreads();  // the list; and every decision is made
+    const bool enough = found >= takes;
+    if (take && enough) {
+        const int page = list[rank];
+        p.table[r.at] = page;
+        p.refs[page] = 1;
+        if (held) atomicSub(p.refs + r.e, 1);
+        if (copy) {
+            p.moves[2 * c] = r.e;
+            p.moves[2 * c + 1] = page;
+        }
+    }
+    if (held) {
+        p.asked[r.e] = 0;
+        p.last[r.e] = 0;
+    }
+    if (tid == 0) {
+        p.counts[0] = enough ? both >> 16 : 0;
+        p.counts[2] = takes;
+        if (!enough) atomicOr(p.status, UAA_DEVFLAG_POOL);
+    }
 }
 
 __global__ void __launch_bounds__(kScanThreads) reserve_kernel(const PageParams p, int q_len)
@@ -280,9 +383,9 @@ __global__ void __launch_bounds__(kScanThreads) compact_kernel(const PageParams 
     __shared__ int buf[33];
     grid_dependency_wait();
     const int tid = threadIdx.x;
+    int r[kScanPer];
     int mine = 0, live;
     for (int64_t i0 = 0; i0 < p.n_pages; i0 += kScanThreads * kScanPer) {
-        int r[kScanPer];
         load_refs(p, i0 + static_cast<int64_t>(tid) * kScanPer, r);
 #pragma unroll
         for (int k = 0; k < kScanPer; ++k) mine += r[k] != 0 && i0 + static_cast<int64_t>(tid) * kScanPer + k < p.n_pages;
@@ -291,8 +394,7 @@ __global__ void __launch_bounds__(kScanThreads) compact_kernel(const PageParams 
     int holes = 0, movers = 0;
     for (int64_t i0 = 0; i0 < p.n_pages; i0 += kScanThreads * kScanPer) {
         const int64_t first = i0 + static_cast<int64_t>(tid) * kScanPer;
-        int r[kScanPer];
-        load_refs(p, first, r);
+        if (p.n_pages > kScanThreads * kScanPer) load_refs(p, first, r);  // else they are the ones just counted
         int nh = 0, nm = 0;
 #pragma unroll
         for (int k = 0; k < kScanPer; ++k) {
@@ -304,13 +406,23 @@ __global__ void __launch_bounds__(kScanThreads) compact_kernel(const PageParams 
         int th, tm;
         int h = holes + block_prefix(nh, buf, th);
         int m = movers + block_prefix(nm, buf, tm);
+        int to[kScanPer];
 #pragma unroll
         for (int k = 0; k < kScanPer; ++k) {
             const int page = static_cast<int>(first) + k;
+            to[k] = r[k] != 0 && page < live ? page : -1;
             if (first + k >= p.n_pages) continue;
             if (r[k] == 0 && page < live) p.moves[2 * h++ + 1] = page;
             if (r[k] != 0 && page >= live) p.moves[2 * m++] = page;
-            p.map[page] = r[k] != 0 && page < live ? page : -1;
+        }
+        if (first + kScanPer <= p.n_pages) {
+#pragma unroll
+            for (int k = 0; k < kScanPer / 4; ++k)
+                reinterpret_cast<int4*>(p.map + first)[k] = make_int4(to[4 * k], to[4 * k + 1], to[4 * k + 2], to[4 * k + 3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kScanPer; ++k)
+                if (first + k < p.n_pages) p.map[first + k] = to[k];
         }
         holes += th;
         movers += tm;
@@ -318,10 +430,11 @@ __global__ void __launch_bounds__(kScanThreads) compact_kernel(const PageParams 
     __threadfence_block();
     __syncthreads();
     for (int i = tid; i < movers; i += kScanThreads) {  // as many holes as movers
-        const int src = p.moves[2 * i], dst = p.moves[2 * i + 1];
-        p.map[src] = dst;
-        p.refs[dst] = p.refs[src];
-        p.refs[src] = 0;
+        const int2 mv = reinterpret_cast<const int2*>(p.moves)[i];
+        const int n = p.refs[mv.x];
+        p.map[mv.x] = mv.y;
+        p.refs[mv.y] = n;
+        p.refs[mv.x] = 0;
     }
     if (tid == 0) {
         p.counts[0] = movers;
@@ -391,6 +504,8 @@ dim3 entries_grid(const PageParams& p)
 
 cudaError_t launch_pages_fork(const PageParams& p, const int* parents, cudaStream_t s)
 {
+    if (static_cast<int64_t>(p.B) * p.per_seq <= kForkEntries)
+        return launch_dependent(fork_small_kernel, dim3(1), dim3(kForkThreads), 0, s, p, parents);
     const cudaError_t e = launch_dependent(fork_gather_kernel, entries_grid(p), dim3(kPageThreads), 0, s, p, parents);
     if (e != cudaSuccess) return e;
     return launch_dependent(fork_scatter_kernel, entries_grid(p), dim3(kPageThreads), 0, s, p);
@@ -403,7 +518,9 @@ cudaError_t launch_pages_trim(const PageParams& p, int window, int first_tokens,
 
 cudaError_t launch_pages_reserve(const PageParams& p, int q_len, cudaStream_t s)
 {
-    return launch_dependent(reserve_kernel, dim3(1), dim3(kScanThreads), 0, s, p, q_len);
+    const int64_t n_req = static_cast<int64_t>(p.B) * ((q_len - 1) / p.page_size + 2);
+    auto* kern = n_req <= kScanThreads ? reserve_small_kernel : reserve_kernel;
+    return launch_dependent(kern, dim3(1), dim3(kScanThreads), 0, s, p, q_len);
 }
 
 cudaError_t launch_pages_compact(const PageParams& p, cudaStream_t s)

@@ -17,7 +17,8 @@ _TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
 def _require_cuda(device):
     if not torch.cuda.is_available():
         raise RuntimeError("DecodeLayer needs a CUDA device; libuaa has no CPU implementation")
-    return torch.device(device)
+    d = torch.device(device)
+    return d if d.index is not None or d.type != "cuda" else torch.device("cuda", torch.cuda.current_device())
 
 
 class DecodeLayer:
@@ -34,6 +35,7 @@ class DecodeLayer:
                  n_pages=None, max_q_len=1, cache=None):
         self.cfg = dict(cfg)
         self.device = _require_cuda(device)
+        self._index = self.device.index
         self.batch = int(batch)
         self.capacity = int(capacity)
         self.desc = B.make_desc(cfg)
@@ -78,6 +80,9 @@ class DecodeLayer:
         if any(t is not None for t in cache.values()):
             raise ValueError(f"a {kv} layer has no cache tensor named {sorted(cache)}")
         self.max_len_hint = 0
+        self._args_cache = {}
+        self._read_args = None
+        self._reads = {}            # read_rows' tensors per row count
         self.out = torch.empty((batch, Hq, D), dtype=_TORCH_DTYPE[cfg.get("out_dtype", "f32")], device=dev)
         self._outs = {1: self.out}  # per tokens-per-step count: [B][Hq][D], or [B][T][Hq][D]
         self.q_len = 1              # tokens per sequence of the current step
@@ -190,14 +195,17 @@ class DecodeLayer:
         msl = self.max_len_hint if max_seq_len is None else int(max_seq_len)
         if out is None:
             out = self.out_for(self.q_len)
+        # a copy: callers may change fields
+        return B.UaaStepArgs.from_buffer_copy(self._args(q, k_new, v_new, msl, q_rot, out))
+
+    def _args(self, q, k_new, v_new, msl, q_rot, out) -> B.UaaStepArgs:
         key = (B.ptr(q), B.ptr(k_new), B.ptr(v_new), msl, B.ptr(q_rot), B.ptr(out), self.q_len)
-        cache = self.__dict__.setdefault("_args_cache", {})
-        a = cache.get(key)
+        a = self._args_cache.get(key)
         if a is None:
-            if len(cache) > 64:
-                cache.clear()
-            a = cache[key] = self._build_args(q, k_new, v_new, msl, q_rot, out)
-        return B.UaaStepArgs.from_buffer_copy(a)  # a copy: callers may change fields
+            if len(self._args_cache) > 64:
+                self._args_cache.clear()
+            a = self._args_cache[key] = self._build_args(q, k_new, v_new, msl, q_rot, out)
+        return a
 
     def _build_args(self, q, k_new, v_new, max_seq_len, q_rot, out) -> B.UaaStepArgs:
         a = B.UaaStepArgs()
@@ -221,12 +229,13 @@ class DecodeLayer:
         """One step (append, split-K partials, combine) on `stream` for q of one token
         per sequence ([B][Hq][D]) or T tokens ([B][T][Hq][D], causal within the
         chunk); the output rows ([B][Hq][D] or [B][T][Hq][D]) go to `out` if given."""
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        s = stream if stream is not None else B.current_stream(self._index)
         T = self._begin(q)
         want = self.out_for(T)
         if out is not None:
             assert out.shape == want.shape and out.dtype == want.dtype and out.is_contiguous()
-        B.uaa_decode_attn(self.desc, self.args(q, k_new, v_new, max_seq_len, q_rot=q_rot, out=out), self.ws, s)
+        msl = self.max_len_hint if max_seq_len is None else int(max_seq_len)
+        B.uaa_decode_attn(self.desc, self._args(q, k_new, v_new, msl, q_rot, want if out is None else out), self.ws, s)
         if advance_hint and max_seq_len is None:
             self.max_len_hint += T
         return want if out is None else out
@@ -235,19 +244,23 @@ class DecodeLayer:
         """The cached keys and values of positions start[b] .. start[b] + n - 1 of every
         sequence (start: int32 tensor [B] on the device, or None for 0), as
         [B][n][Hkv][D] tensors in the layer's out dtype; any cache kind, paged or not.
-        Positions outside the cache, or on absent pages, read as zeros."""
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        if start is not None and (tuple(start.shape) != (self.batch,) or start.dtype != torch.int32
+        Positions outside the cache, or on absent pages, read as zeros. The tensors are
+        the layer's own (one pair per n), overwritten by the next read of n rows, as a
+        step's output is by the next step."""
+        s = stream if stream is not None else B.current_stream(self._index)
+        if start is not None and (start.dtype is not torch.int32 or start.shape != self.seq_lens.shape
                                   or not start.is_cuda or not start.is_contiguous()):
             raise ValueError("start is not a contiguous int32 tensor [batch] on the device")
-        shape = (self.batch, int(n), self.cfg["n_kv_heads"], self.cfg["head_dim"])
-        k = torch.empty(shape, dtype=self.out.dtype, device=self.device)
-        v = torch.empty_like(k)
-        a = self.__dict__.get("_read_args")
-        if a is None:
-            a = self._read_args = self._build_args(None, None, None, 0, None, None)
-        B.uaa_cache_read(self.desc, a, B.ptr(start), int(n), B.ptr(k), B.ptr(v), s)
-        return k, v
+        got = self._reads.get(n)
+        if got is None:
+            if len(self._reads) > 16:
+                self._reads.clear()
+            shape = (self.batch, int(n), self.cfg["n_kv_heads"], self.cfg["head_dim"])
+            got = self._reads[n] = tuple(torch.empty(shape, dtype=self.out.dtype, device=self.device) for _ in "kv")
+        if self._read_args is None:
+            self._read_args = self._build_args(None, None, None, 0, None, None)
+        B.uaa_cache_read(self.desc, self._read_args, B.ptr(start), int(n), B.ptr(got[0]), B.ptr(got[1]), s)
+        return got
 
     def append(self, q, k_new, v_new, stream=None, q_rot=None):
         s = stream if stream is not None else torch.cuda.current_stream(self.device)

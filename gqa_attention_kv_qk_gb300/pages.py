@@ -31,7 +31,8 @@ class PageTable:
     def __init__(self, block_table, page_size: int, n_pages: int, page_refs=None, seq_lens=None, device="cuda"):
         if not torch.cuda.is_available():
             raise RuntimeError("PageTable needs a CUDA device; libuaa has no CPU implementation")
-        self.device = dev = torch.device(device)
+        dev = torch.device(device)
+        self.device = dev = dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
         to = lambda t: torch.as_tensor(t, dtype=torch.int32).to(dev).contiguous()
         self.block_table = to(block_table)
         if self.block_table.dim() != 2:
@@ -62,11 +63,11 @@ class PageTable:
         a.moves, a.counts = B.ptr(self.moves), B.ptr(self.counts)
 
     def _s(self, stream):
-        return stream if stream is not None else torch.cuda.current_stream(self.device)
+        return stream if stream is not None else B.current_stream(self.device.index)
 
     def fork(self, parents, stream=None):
         """Row b becomes a copy of row parents[b] (int32 [batch] on the device; -1: it ends)."""
-        if (tuple(parents.shape) != (self.batch,) or parents.dtype != torch.int32 or not parents.is_cuda
+        if (parents.dtype is not torch.int32 or parents.shape != self.seq_lens.shape or not parents.is_cuda
                 or not parents.is_contiguous()):
             raise ValueError("parents is not a contiguous int32 tensor [batch] on the device")
         B.uaa_pages_fork(self.args, B.ptr(parents), self.ws, self._s(stream))
@@ -85,13 +86,14 @@ class PageTable:
 
     def copy(self, *pools, stream=None):
         """The copies of the last reserve() or compact() in pools [n_pages][...] (up to eight)."""
-        sizes = []
+        n, ptrs, sizes = self.n_pages, [], []
         for t in pools:
-            if t.shape[0] != self.n_pages or not t.is_contiguous() or not t.is_cuda:
-                raise ValueError(f"a pool is {tuple(t.shape)} on {t.device}, not a contiguous [{self.n_pages}][...] "
-                                 "tensor on the device")
-            sizes.append(t.numel() // self.n_pages * t.element_size())
-        B.uaa_pages_copy(self.args, [B.ptr(t) for t in pools], sizes, self.ws, self._s(stream))
+            if t.size(0) != n or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"a pool is {tuple(t.shape)} on {t.device}, not a contiguous [{n}][...] tensor on "
+                                 "the device")
+            ptrs.append(t.data_ptr())
+            sizes.append(t.nbytes // n)
+        B.uaa_pages_copy(self.args, ptrs, sizes, self.ws, self._s(stream))
 
     def copy_layer(self, layer, stream=None):
         """copy() for a DecodeLayer's caches and their scales."""
