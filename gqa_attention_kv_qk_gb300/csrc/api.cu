@@ -110,6 +110,10 @@ uaa_status check_desc(const uaa_attn_desc* d)
 // Tokens per sequence one step takes at most (a prefill chunk).
 constexpr int kMaxQLen = 1024;
 
+// Workspace that a prefill chunk over a 4-bit cache takes for widened rows, at most
+// (more only where one sequence needs it).
+constexpr size_t kDenseBytes = (size_t)512 << 20;
+
 struct Plan {
     int G;
     int q_len;           // tokens per sequence (1: decode)
@@ -123,7 +127,9 @@ struct Plan {
     int n_slices;
     int per_sm;          // resident CTAs per SM
     int prefill;         // a contiguous cache takes the query-tiled prefill kernel (no combine)
-    size_t off_status, off_qrot, off_prefix, off_rec_lse, off_rec_o, off_ranges, off_owners, off_balance, total;
+    int dense_rows;      // 4-bit caches there: rows per (sequence, kv head) widened in the workspace,
+    int dense_batch;     // for so many sequences at a time (0 rows: other caches)
+    size_t off_status, off_qrot, off_prefix, off_rec_lse, off_rec_o, off_ranges, off_owners, off_balance, off_dense, total;
     size_t prefix_stride, rec_lse_stride, rec_o_stride, ranges_stride, owners_stride;  // bytes per slice
 };
 
@@ -191,14 +197,12 @@ uaa_status make_plan(const uaa_attn_desc* d, int batch, int q_len, int max_len, 
     }
     p.head_groups = (rows + p.heads_per_cta - 1) / p.heads_per_cta;
     p.mg = p.kernel == 1 ? uaa::partial_tc_keys_per_stage(d->head_dim, d->kv_dtype, p.n_head_tiles) / uaa::kTileKeys : 1;
-    // tensor-core kernel: two CTAs per SM, one at head_dim 256 and with two column
-    // tiles (its eight consumer warps take the registers of two CTAs)
-    p.per_sm = p.kernel == 0 ? 4 : (d->head_dim == 256 || p.n_head_tiles == 2 ? 1 : 2);
+    p.per_sm = p.kernel == 0 ? 4 : uaa::partial_tc_ctas_per_sm(d->head_dim, d->kv_dtype, p.n_head_tiles);
     p.n_ctas = n_sm * p.per_sm;
     // long chunks on contiguous bf16 caches: whole 64-row blocks of (token, head) rows
     // per CTA, each streaming its keys once (the partial kernel's units hold 16 rows)
-    p.prefill = p.kernel == 1 && d->kv_dtype == UAA_DTYPE_BF16 && (d->head_dim == 64 || d->head_dim == 128) &&
-                rows >= uaa::kPrefillRows;
+    p.prefill = p.kernel == 1 && (d->kv_dtype == UAA_DTYPE_BF16 || d->kv_dtype == UAA_DTYPE_Q4) &&
+                (d->head_dim == 64 || d->head_dim == 128) && rows >= uaa::kPrefillRows;
     p.slice = batch < uaa::kMaxSliceBatch ? (batch > 0 ? batch : 1) : uaa::kMaxSliceBatch;
     p.n_slices = batch > 0 ? (batch + p.slice - 1) / p.slice : 0;
 
@@ -218,6 +222,29 @@ uaa_status make_plan(const uaa_attn_desc* d, int batch, int q_len, int max_len, 
     p.off_ranges = p.off_rec_o + p.n_slices * p.rec_o_stride;
     p.off_owners = p.off_ranges + p.n_slices * p.ranges_stride;
     p.total = p.off_owners + p.n_slices * p.owners_stride;
+    if (p.prefill && d->kv_dtype == UAA_DTYPE_Q4) {
+        // the visible rows of as many sequences as kDenseBytes hold (one at least),
+        // widened to fp16: keys, then values
+        const long long rows_max = 2147483647LL - 2 * uaa::kTileKeys;
+        const long long per_head = ((long long)max_len + p.q_len + 63) / 64 * 64;
+        if (per_head * d->n_kv_heads > rows_max)
+            return fail(UAA_ERR_UNSUPPORTED, "(max_seq_len + q_len) * n_kv_heads=%lld exceeds 2^31 cache rows",
+                        per_head * d->n_kv_heads);
+        const size_t per_seq = (size_t)per_head * d->n_kv_heads * D * 4;
+        const size_t whole = B * per_seq, limit = per_seq > kDenseBytes ? per_seq : kDenseBytes;
+        const size_t dense = whole < limit ? whole : limit;
+        long long nb = per_seq ? (long long)(dense / per_seq) : 0;
+        const long long by_grid = 65535 / d->n_kv_heads, by_rows = rows_max / (per_head * d->n_kv_heads);
+        if (nb > by_grid) nb = by_grid;
+        if (nb > by_rows) nb = by_rows;
+        if (B > 0 && nb < 1)
+            return fail(UAA_ERR_UNSUPPORTED, "n_kv_heads=%d is above 65535 for a chunk over a 4-bit cache",
+                        d->n_kv_heads);
+        p.dense_rows = (int)per_head;
+        p.dense_batch = (int)nb;
+        p.off_dense = align256(p.total);
+        p.total = p.off_dense + dense;
+    }
     *pl = p;
     return UAA_OK;
 }
@@ -385,7 +412,7 @@ float qscale(const uaa_attn_desc* d)
 // Entries of pairs beyond R/2 stay 0 (those pairs are not rotated).
 int rotary_dims(const uaa_attn_desc* d) { return d->rotary_dim > 0 ? d->rotary_dim : d->head_dim; }
 
-void rope_table(const uaa_attn_desc* d, double* inv_freq_over_pi, float* mscale, double* mscale64 = nullptr)
+void make_rope_table(const uaa_attn_desc* d, double* inv_freq_over_pi, double* mscale)
 {
     const int D = rotary_dims(d);
     for (int i = 0; i < d->head_dim / 2; ++i) inv_freq_over_pi[i] = 0.0;
@@ -422,8 +449,34 @@ void rope_table(const uaa_attn_desc* d, double* inv_freq_over_pi, float* mscale,
         }
         inv_freq_over_pi[i] = g / pi;
     }
-    *mscale = (float)ms;
-    if (mscale64) *mscale64 = ms;
+    *mscale = ms;
+}
+
+// The table of the descriptor, kept from the thread's last call with the same rotary
+// facts (64 pow take longer than a launch).
+void rope_table(const uaa_attn_desc* d, double* inv_freq_over_pi, float* mscale, double* mscale64 = nullptr)
+{
+    struct Kept {
+        bool valid;
+        int head_dim, rotary_dim;
+        uaa_rope_params rope;
+        double table[uaa::kMaxHeadDim / 2], mscale;
+    };
+    static thread_local Kept k = {};
+    const uaa_rope_params &a = k.rope, &b = d->rope;
+    if (!k.valid || k.head_dim != d->head_dim || k.rotary_dim != d->rotary_dim || a.theta != b.theta ||
+        a.scaling != b.scaling || a.factor != b.factor || a.low_freq_factor != b.low_freq_factor ||
+        a.high_freq_factor != b.high_freq_factor || a.original_max_pos != b.original_max_pos ||
+        a.beta_fast != b.beta_fast || a.beta_slow != b.beta_slow || a.attn_factor != b.attn_factor) {
+        make_rope_table(d, k.table, &k.mscale);
+        k.head_dim = d->head_dim;
+        k.rotary_dim = d->rotary_dim;
+        k.rope = d->rope;
+        k.valid = true;
+    }
+    memcpy(inv_freq_over_pi, k.table, sizeof(double) * (d->head_dim / 2));
+    *mscale = (float)k.mscale;
+    if (mscale64) *mscale64 = k.mscale;
 }
 
 // ---------------------------------------------------------------- TMA descriptors
@@ -512,13 +565,80 @@ uaa_status run_append(const uaa_attn_desc* d, const uaa_step_args* a, const uaa_
 }
 
 // The query-tiled prefill kernel takes step 2 of this call (and step 3 has nothing to do).
-bool takes_prefill(const uaa_step_args* a, const Plan& pl) { return pl.prefill && !a->block_table; }
+bool takes_prefill(const uaa_step_args* a, const Plan& pl)
+{
+    return pl.prefill && (!a->block_table || pl.dense_rows > 0);
+}
+
+// A prefill chunk over a 4-bit cache: the rows that it sees widened to fp16, then the
+// prefill kernel on them, as many sequences at a time as the workspace holds.
+uaa_status run_prefill_q4(const uaa_attn_desc* d, const uaa_step_args* a, const uaa_workspace* ws, const Plan& pl,
+                          cudaStream_t s)
+{
+    char* w = static_cast<char*>(ws->ptr);
+    const uint64_t D = d->head_dim;
+    const size_t q_rows = (size_t)pl.q_len * d->n_q_heads * D;
+    const size_t out_elem = d->out_dtype == UAA_DTYPE_F32 ? 4 : 2;
+    for (int b0 = 0; b0 < a->batch; b0 += pl.dense_batch) {
+        const int nb = a->batch - b0 < pl.dense_batch ? a->batch - b0 : pl.dense_batch;
+        const uint64_t rows = (uint64_t)nb * d->n_kv_heads * pl.dense_rows;
+        uaa::WidenParams wp{};
+        wp.B = nb;
+        wp.Hkv = d->n_kv_heads;
+        wp.D = d->head_dim;
+        wp.cap = a->cache_capacity;
+        wp.row_cap = pl.dense_rows;
+        wp.b_off = b0;
+        wp.q_len = pl.q_len;
+        wp.window = partition_window(d, pl);
+        wp.first_tokens = first_tokens(d);
+        wp.seq_lens = a->seq_lens + b0;
+        wp.k_cache = a->k_cache;
+        wp.v_cache = a->v_cache;
+        wp.k_scale = a->k_scale;
+        wp.v_scale = a->v_scale;
+        wp.pages = pages_of(a);
+        if (!a->block_table) wp.pages.table = nullptr;
+        wp.k_out = w + pl.off_dense;
+        wp.v_out = w + pl.off_dense + rows * D * 2;
+        wp.status = reinterpret_cast<unsigned*>(w + pl.off_status);
+        cudaError_t e = uaa::launch_widen_q4(wp, s);
+        if (e != cudaSuccess) return cuda_fail(e, "4-bit widening kernel launch");
+        CUtensorMap tk, tv;
+        UAA_TRY(encode_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, wp.k_out, D, rows, D * 2, 64,
+                          (uint32_t)uaa::kPrefillKeys, CU_TENSOR_MAP_SWIZZLE_128B, "widened keys"));
+        UAA_TRY(encode_2d(&tv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, wp.v_out, D, rows, D * 2, 64,
+                          (uint32_t)uaa::kPrefillKeys, CU_TENSOR_MAP_SWIZZLE_128B, "widened values"));
+        uaa::PrefillParams p{};
+        p.B = nb;
+        p.Hq = d->n_q_heads;
+        p.Hkv = d->n_kv_heads;
+        p.D = d->head_dim;
+        p.G = pl.G;
+        p.q_len = pl.q_len;
+        p.cap = a->cache_capacity;
+        p.row_cap = pl.dense_rows;
+        p.window = d->window;
+        p.first_tokens = first_tokens(d);
+        p.softcap_log2e = d->softcap > 0.f ? d->softcap * uaa::kLog2e : 0.f;
+        p.q_prime = reinterpret_cast<const float*>(w + pl.off_qrot) + b0 * q_rows;
+        p.seq_lens = a->seq_lens + b0;
+        p.sink = d->has_sink ? a->sink : nullptr;
+        p.out = static_cast<char*>(a->out) + b0 * q_rows * out_elem;
+        p.out_dtype = d->out_dtype;
+        p.status = reinterpret_cast<unsigned*>(w + pl.off_status);
+        e = uaa::launch_prefill_umma(p, tk, tv, s);
+        if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");
+    }
+    return UAA_OK;
+}
 
 uaa_status run_prefill(const uaa_attn_desc* d, const uaa_step_args* a, const uaa_workspace* ws, const Plan& pl,
                        cudaStream_t s)
 {
     char* w = static_cast<char*>(ws->ptr);
     const uint64_t D = d->head_dim;
+    if (pl.dense_rows > 0) return run_prefill_q4(d, a, ws, pl, s);
     const uint64_t rows = (uint64_t)a->batch * d->n_kv_heads * a->cache_capacity;
     CUtensorMap tk, tv;
     UAA_TRY(encode_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->k_cache, D, rows, D * 2, 64,
@@ -984,6 +1104,7 @@ uaa_status uaa_get_workspace_layout(const uaa_attn_desc* desc, int32_t batch, in
         layout->step_splits = f32_step_splits(desc, &a, pl);
         layout->step_kernels = batch == 0 ? 0
                                : layout->step_splits > 0 ? 1
+                               : pl.dense_rows > 0 ? 1 + 2 * ((batch + pl.dense_batch - 1) / pl.dense_batch)
                                : pl.prefill ? 2
                                : (pl.kernel == 1 && pl.q_len == 1) ? 2 * pl.n_slices
                                                                    : 1 + 2 * pl.n_slices;

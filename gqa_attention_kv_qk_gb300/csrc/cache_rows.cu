@@ -1,6 +1,7 @@
-// cache_rows.cu -- rows on their way into and out of a cache outside a step: the
-// 4-bit quantiser that fills a cache from existing values, and the reader that
-// gives cached rows back as values. Both stream: each value is read once and
+// cache_rows.cu -- rows on their way into and out of a cache outside a step's
+// attention: the 4-bit quantiser that fills a cache from existing values, the
+// reader that gives cached rows back as values, and the widening of a 4-bit cache's
+// visible rows to fp16 for a prefill chunk. All stream: each value is read once and
 // written once, a thread takes 16 (quantise) or 8 (read) neighbouring values with
 // 16-byte accesses, and HBM is the bound for anything beyond a few hundred rows.
 #include "internal.cuh"
@@ -139,7 +140,71 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const ReadParam
     store8(out, p.out_dtype, static_cast<size_t>(i) * 8, x);
 }
 
+// A CTA per 64 rows of (sequence, kv head), keys (blockIdx.z 0) or values: a thread
+// takes 16 values (8 bytes of codes) at a time. Rows in 128-row blocks (the prefill
+// kernel's) that no token of the chunk sees are left alone; in the others rows that
+// none sees, or without a page, are zeros.
+constexpr int kWidenRows = 64;
+
+__global__ void __launch_bounds__(kRowThreads) widen_q4_kernel(const WidenParams p)
+{
+    grid_dependency_wait();  // the append's rows and lengths are complete
+    const int row0 = blockIdx.x * kWidenRows;
+    const int bh = blockIdx.y, b = bh / p.Hkv, h = bh - b * p.Hkv;
+    const bool is_v = blockIdx.z == 1;
+    const int n = p.seq_lens[b];
+    const int L = n - p.q_len;
+    if (n > p.row_cap) {  // longer than the caller's bound: the prefill kernel leaves zero rows
+        if (blockIdx.x == 0 && h == 0 && !is_v && threadIdx.x == 0 && n <= p.cap)
+            atomicOr(p.status, UAA_DEVFLAG_LEN_HINT);
+        return;
+    }
+    if (L < 0 || row0 >= n) return;
+    const Keys keys = key_range(n, p.window, p.first_tokens);  // the chunk's union
+    const int block = row0 / kPrefillKeys * kPrefillKeys;
+    if (block + kPrefillKeys <= keys.lo && block >= keys.first) return;
+    const void* cache = is_v ? p.v_cache : p.k_cache;
+    const __half* scale = reinterpret_cast<const __half*>(is_v ? p.v_scale : p.k_scale);
+    __half* out = static_cast<__half*>(is_v ? p.v_out : p.k_out) + static_cast<size_t>(bh) * p.row_cap * p.D;
+    const int per_row = p.D / 16;
+    for (int i = threadIdx.x; i < kWidenRows * per_row; i += kRowThreads) {
+        const int r = row0 + i / per_row, e = i % per_row;
+        if (r >= n) break;
+        const bool seen = r < keys.first || r >= keys.lo;
+        const long long row = seen ? cache_row(p.pages, p.Hkv, p.cap, p.b_off + b, h, r) : -1;
+        uint2 c = make_uint2(0x88888888u, 0x88888888u);  // code 0
+        __half2 s = __half2half2(__float2half_rn(0.f));
+        if (row >= 0) {
+            c = reinterpret_cast<const uint2*>(cache)[row * per_row + e];
+            s = __half2half2(scale[row * (p.D / 32) + e / 2]);
+        } else if (seen && e == 0) {
+            atomicOr(p.status, UAA_DEVFLAG_PAGE);
+        }
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t u = ((j < 4 ? c.x : c.y) >> (8 * (j & 3))) & 0xffu;
+            const __half2 v = __floats2half2_rn(static_cast<float>(u & 15u) - 8.f, static_cast<float>(u >> 4) - 8.f);
+            const __half2 x = __hmul2(v, s);  // exact: 3 bits times 8
+            memcpy(&w[j], &x, 4);
+        }
+        uint4* o = reinterpret_cast<uint4*>(out + static_cast<size_t>(r) * p.D + 16 * e);
+        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_widen_q4(const WidenParams& p, cudaStream_t s)
+{
+    if (p.B == 0) return cudaSuccess;
+    if (static_cast<long long>(p.B) * p.Hkv > 65535) return cudaErrorInvalidConfiguration;
+    return launch_dependent(widen_q4_kernel,
+                            dim3(static_cast<unsigned>((p.row_cap + kWidenRows - 1) / kWidenRows),
+                                 static_cast<unsigned>(p.B * p.Hkv), 2),
+                            dim3(kRowThreads), 0, s, p);
+}
 
 cudaError_t launch_q4_quantize(const void* x, int dtype, int64_t n_rows, int D, uint8_t* codes, __half* scales,
                                cudaStream_t s)

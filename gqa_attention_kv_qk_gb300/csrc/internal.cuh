@@ -220,8 +220,8 @@ struct StepF32Params {
 
 // Attention of a long chunk (prefill_umma.cu), after the append: a CTA per
 // (sequence, kv head, block of 128 (token, head) rows) streams the keys its rows
-// see once and writes their output rows; contiguous bf16 caches, head_dim 64 or
-// 128.
+// see once and writes their output rows; contiguous bf16 caches, or the rows of a
+// 4-bit cache widened to fp16 (row_cap > 0), head_dim 64 or 128.
 struct PrefillParams {
     int B, Hq, Hkv, D, G;
     int q_len;              // tokens per sequence
@@ -231,6 +231,7 @@ struct PrefillParams {
     float softcap_log2e;    // 0: no softcap; else softcap * log2(e)
     const float* q_prime;   // [B][q_len][Hq][D], written by the append
     const int* seq_lens;    // lengths after the append
+    int row_cap;            // widened rows per (sequence, kv head); 0: the bf16 cache itself
     const float* sink;      // [Hq] or null
     void* out;              // [B][q_len][Hq][D]
     int out_dtype;
@@ -283,6 +284,24 @@ struct ReadParams {
 };
 cudaError_t launch_cache_read(const ReadParams& p, cudaStream_t s);
 
+// The rows of a 4-bit cache that a chunk of q_len tokens sees, widened to fp16
+// (cache_rows.cu): [B][Hkv][row_cap][D] keys, then values.
+struct WidenParams {
+    int B, Hkv, D, cap, row_cap;
+    int b_off;              // first sequence (rows of the cache and the table)
+    int q_len, window, first_tokens;
+    const int* seq_lens;    // [B] lengths after the append (already offset)
+    const void* k_cache;
+    const void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    KvPages pages;
+    void* k_out;
+    void* v_out;
+    unsigned* status;
+};
+cudaError_t launch_widen_q4(const WidenParams& p, cudaStream_t s);
+
 // The pages of a paged cache (pages.cu).
 struct PageParams {
     int B, per_seq, page_size, n_pages;
@@ -321,6 +340,8 @@ size_t partial_tc_smem_bytes(int D, int kv_dtype, int n_head_tiles);
 // Keys per ring stage of the tensor-core partial kernel (the TMA box height) for
 // n_head_tiles 8-row column tiles per unit.
 int partial_tc_keys_per_stage(int D, int kv_dtype, int nht);
+// Its CTAs per SM.
+int partial_tc_ctas_per_sm(int D, int kv_dtype, int nht);
 // Largest batch slice one partial launch takes (its stage prefix lives in shared memory).
 constexpr int kMaxSliceBatch = 1024;
 

@@ -33,6 +33,8 @@ int partial_tc_keys_per_stage(int D, int kv_dtype, int nht)
     }
 }
 
+int partial_tc_ctas_per_sm(int D, int kv_dtype, int nht) { return ctas_per_sm(D, kv_kind(kv_dtype), nht); }
+
 size_t partial_tc_smem_bytes(int D, int kv_dtype, int n_head_tiles)
 {
     switch (kv_kind(kv_dtype)) {

@@ -72,9 +72,12 @@ namespace {
 // of every stage. With one 8-column tile there are four consumer warps; with two
 // there are eight, warp w serving tile w / 4, so no warp holds both tiles'
 // state. The producer and the prep warp follow the consumers.
+//
+// Over a 4-bit cache a warp serves both tiles of its keys: widening the codes costs
+// more than the contractions, so each key is widened once. (More consumer warps do
+// not help there: with 6 or 8 key groups of fewer registers each, 12 or 16 warps an
+// SM, the 8K decode ran 53-56 us against 50.)
 constexpr int kKeyGroups = 4;
-__host__ __device__ constexpr int consumer_warps(int nht) { return nht == 2 ? 8 : 4; }
-__host__ __device__ constexpr int cta_threads(int nht) { return (consumer_warps(nht) + 2) * 32; }
 
 __host__ __device__ constexpr int round_up(int x, int a) { return (x + a - 1) / a * a; }
 
@@ -83,16 +86,28 @@ __host__ __device__ constexpr int round_up(int x, int a) { return (x + a - 1) / 
 // (4-bit codes for both, a scale per key and 32 dims).
 constexpr int kKvBf16 = 0, kKvVq8 = 1, kKvQ8 = 2, kKvQ4 = 3;
 
+// CTAs per SM: two, but one at head_dim 256 and with two column tiles (4-bit caches:
+// where a warp's state is that large), whose warps take the registers of two.
+__host__ __device__ constexpr int ctas_per_sm(int D, int KV, int NHT)
+{
+    if (KV == kKvQ4) return D * NHT <= 128 ? 2 : 1;
+    return D == 256 || NHT == 2 ? 1 : 2;
+}
+
 // MG: 16-key groups each consumer warp takes per stage: where a key costs few
 // bytes the consumers, not HBM, set the pace, and MG independent QK chains per
 // warp hide their latency. Head_dim 64: 2 for bf16, 4 for vq8 and q8 (one
 // 256-key stage); q8 at head_dims 128 and 256: 2 (a q8 key row is half a bf16
 // one: with one group its consumers measured 15 % slower); two column tiles at
 // head_dim 128: 2 (each key feeds twice the MMAs; one CTA per SM has room for
-// three 128-key stages; 6-16 % faster than one group).
+// three 128-key stages; 6-16 % faster than one group). 4-bit caches take their
+// groups in turn: 4 of them (2 at head_dim 256, where a box of scales holds no
+// more keys) share a stage's waits, 4 % faster than 2 at head_dim 128.
 template <int D, int KV, int NHT = 1>
 struct KeyGroups {
-    static constexpr int kMG = D == 64 ? (KV != kKvBf16 ? 4 : 2) : (KV >= kKvQ8 || NHT == 2 ? 2 : 1);
+    static constexpr int kMG = KV == kKvQ4 ? (D == 256 ? 2 : 4)
+                               : D == 64   ? (KV != kKvBf16 ? 4 : 2)
+                                           : (KV == kKvQ8 || NHT == 2 ? 2 : 1);
 };
 
 // Shared memory, from a 1024-byte aligned base: the ring of kStages stages |
@@ -102,6 +117,10 @@ struct KeyGroups {
 template <int D, int KV, int NHT>
 struct Shape {
     static constexpr int kD = D;
+    static constexpr int kTilesPerWarp = KV == kKvQ4 ? NHT : 1;              // 8-column tiles of a consumer warp
+    static constexpr int kConsumers = kKeyGroups * NHT / kTilesPerWarp;     // consumer warps
+    static constexpr int kThreads = (kConsumers + 2) * 32;
+    static constexpr int kPerSM = ctas_per_sm(D, KV, NHT);
     static constexpr bool kVQ8 = KV == kKvVq8 || KV == kKvQ8;  // int8 value codes + scales
     static constexpr bool kKQ8 = KV == kKvQ8;                // int8 key codes + scales
     static constexpr bool kQ4 = KV == kKvQ4;                 // 4-bit key and value codes + scales
@@ -148,7 +167,7 @@ struct Shape {
     static constexpr int kFixedBytes =
         1024 + kCtlBytes + kPrefixBytes + kLensBytes + kFragBytes + 2 * kNewRowBytes + kTabBytes + kNearBytes;
     // one CTA per SM at head_dim 256 and with two column tiles (eight consumer warps)
-    static constexpr int kCtaBudget = D == 256 || NHT == 2 ? 227 * 1024 : 228 * 1024 / 2 - 1024;
+    static constexpr int kCtaBudget = kPerSM == 1 ? 227 * 1024 : 228 * 1024 / kPerSM - 1024;
     static constexpr int kStagesRaw = (kCtaBudget - kFixedBytes) / (kStageBytes + 16);
     static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
     static_assert(kStages >= 2, "a ring of at least two stages");
@@ -228,25 +247,52 @@ __device__ __forceinline__ void widen_code_quad(uint32_t r, uint32_t& d01, uint3
     d23 = hsub2_u32(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
 }
 
-// A register of 4-bit codes holds nibbles 0-3 of two 16-bit halves (values u =
-// code + 8). Returns the fp16 pair of nibble I of both halves as code * s, exactly:
-// u goes into mantissa bits 6-9 of 16 (fp16 0x4C00: 16 + u), and (16 + u) s - 24 s
-// is one fused multiply-add. s has at most 8 significant bits, so 24 s (10 bits)
-// and code * s (11 bits) are fp16 numbers. s: the two halves' scales, s24 = -24 s.
-template <int I>
-__device__ __forceinline__ uint32_t widen_q4(uint32_t r, uint32_t s, uint32_t s24)
+// 4-bit codes, u = code + 8. A register r holds nibbles 0-3 of two 16-bit halves.
+// Nibble 0 of both halves becomes the fp16 pair 1024 + u (mantissa bits 0-3 of
+// 0x6400), nibble 1 the pair 64 + u (bits 4-7 of 0x5400); r >> 8 gives nibbles 2
+// and 3 the same way. So four pairs take one shift and four and-ors of the integer
+// pipe, which bounds the widening (half a warp instruction a cycle); exact fp16
+// subtractions do the rest. The exponents are kept in registers whose value the
+// compiler does not know (q4_exponents): as literals each and-or became two
+// instructions (measured: 72 integer instructions for 8 registers against 42).
+struct Q4Exponents {
+    uint32_t e0, e1;
+};
+
+__device__ __forceinline__ Q4Exponents q4_exponents(const PartialParams& p)
 {
-    const uint32_t u = I == 0 ? r << 6 : I == 1 ? r << 2 : I == 2 ? r >> 2 : r >> 6;
-    uint32_t h = (u & 0x03C003C0u) | 0x4C004C00u;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(h) : "r"(h), "r"(s), "r"(s24));
-    return h;
+    const uint32_t zero = static_cast<uint32_t>(p.D) >> 16;
+    return {0x64006400u + zero, 0x54005400u + zero};
 }
 
-__device__ __forceinline__ uint32_t neg24(uint32_t s)  // -24 s, both halves
+__device__ __forceinline__ uint32_t nibble0(uint32_t r, Q4Exponents e) { return (r & 0x000F000Fu) | e.e0; }
+__device__ __forceinline__ uint32_t nibble1(uint32_t r, Q4Exponents e) { return (r & 0x00F000F0u) | e.e1; }
+
+__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b)
 {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(0xCE00CE00u));
-    return r;
+    __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<uint32_t*>(&r);
+}
+
+// Pairs of 64 + u of nibbles 0-3 (keys: the 72 = 64 + 8 comes off the logits).
+__device__ __forceinline__ void widen_q4_key(uint32_t r, Q4Exponents e, uint32_t (&h)[4])
+{
+    const uint32_t r8 = r >> 8;
+    h[0] = hsub2_u32(nibble0(r, e), 0x63806380u);  // 1024 + u - 960
+    h[1] = nibble1(r, e);
+    h[2] = hsub2_u32(nibble0(r8, e), 0x63806380u);
+    h[3] = nibble1(r8, e);
+}
+
+// Pairs of code * s of nibbles 0-3, exactly (s: the halves' scales, of 8 significant
+// bits; a code has 3).
+__device__ __forceinline__ void widen_q4_value(uint32_t r, uint32_t s, Q4Exponents e, uint32_t (&h)[4])
+{
+    const uint32_t r8 = r >> 8;
+    h[0] = hmul2_u32(hsub2_u32(nibble0(r, e), 0x64086408u), s);   // (1024 + u - 1032) s
+    h[1] = hmul2_u32(hsub2_u32(nibble1(r, e), 0x54805480u), s);   // (64 + u - 72) s
+    h[2] = hmul2_u32(hsub2_u32(nibble0(r8, e), 0x64086408u), s);
+    h[3] = hmul2_u32(hsub2_u32(nibble1(r8, e), 0x54805480u), s);
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
@@ -786,11 +832,193 @@ __device__ __forceinline__ void patch_stage_row(const uint8_t* staging, uint8_t*
     __syncwarp();
 }
 
+// Prep warp, 4-bit keys: -72 times the sum of each q' row's fp16 values over each
+// 32-dim group, as D / 32 floats at 2 D bytes of the fragment row.
+template <int D, int HC>
+__device__ __forceinline__ void q4_group_sums(uint8_t* frag, int row_bytes, int lane)
+{
+    __syncwarp();
+    constexpr int NG = D / 32;
+    for (int i = lane; i < HC * NG; i += 32) {
+        uint8_t* row = frag + (i / NG) * row_bytes;
+        const uint4* q = reinterpret_cast<const uint4*>(row + 64 * (i % NG));
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint4 w = q[k];
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+                sum += f.x + f.y;
+            }
+        }
+        reinterpret_cast<float*>(row + 2 * D)[i % NG] = -72.f * sum;
+    }
+}
+
+// A group of 16 keys of a 4-bit cache for a consumer warp, against its NTW tiles of 8
+// query rows. kaddr, vaddr: this lane's rows for ldmatrix of the keys and values,
+// 16-byte chunk lane / 16 (keys) or lane / 8 % 2 (values); the chunk 2 c further on is
+// the address XOR 32 c (swizzled rows). ksc, vsc: the scales of keys g and 2t. kbase:
+// the position of the first key. GENERAL: keys may be masked, or logits capped.
+//
+// Logits. An ldmatrix.x4 covers 16 keys x 64 dims; register j holds key g (+8 for
+// odd j), dims 8t .. 8t + 7 of 32-dim group 2 kc + j / 2, whose nibble pairs (i, i + 4)
+// are the A operands of two k-steps as 64 + u, u = code + 8 (widen_q4_key). With
+// the accumulator started at -72 sum(q') of the group (bias), a group's contraction
+// is sum q' code, and the logit is the sum over the groups of scale x that, in fp32.
+// 64 + u as the operand keeps sums to a few hundred times q', 2^-24 of which is far
+// below q's own fp16 rounding.
+//
+// Softmax. The reference maximum m is raised only where a logit exceeds it by more
+// than 2^8 (weights then stay below 2^8, sums in fp32): most groups need no exchange
+// between lanes. The weights go to the tensor core as one fp16 part (2^-11).
+//
+// Values. ldmatrix.trans hands a lane the 4 dims 32 c + 4 g .. + 3 (a b16 element)
+// of keys 2t and 2t + 1; nibble i of both is the fp16 pair of dim 4 g + i, widened to
+// code x scale exactly. m-tile 2 c has dims 4 g (row g) and 4 g + 1 (row g + 8) of
+// group c, m-tile 2 c + 1 dims 4 g + 2 and 4 g + 3.
+template <class SH, int NTW, bool FIRST, bool GENERAL>
+__device__ __forceinline__ void consume_q4(const PartialParams& p, uint32_t kaddr, uint32_t vaddr, const uint8_t* ksc,
+                                           const uint8_t* vsc, int kbase, int lo, int hi, bool causal,
+                                           const int (&kmax)[NTW][2], const int (&kmin)[NTW][2],
+                                           const uint32_t (&q)[NTW][SH::kD / 16][2],
+                                           const float (&bias)[NTW][SH::kD / 32][2], Q4Exponents ex, float (&m)[NTW][2],
+                                           float (&l)[NTW][2], float (&o)[NTW][SH::kD / 16][4], int lane)
+{
+    constexpr int D = SH::kD;
+    const int g = lane >> 2, t = lane & 3;
+
+    float x[NTW][4];  // keys g (elements 0, 1) and g + 8 (2, 3), rows 2t and 2t + 1
+    {
+        uint32_t sg[D / 64], sg8[D / 64];  // the scales of keys g and g + 8, two groups a word
+        load_words<D / 64>(ksc, sg);
+        load_words<D / 64>(ksc + 8 * SH::kScaleRow, sg8);
+#pragma unroll
+        for (int kc = 0; kc < D / 64; ++kc) {
+            uint32_t r[4];
+            ptx::ldsm_x4(r, kaddr ^ (32 * kc));
+            const float2 s0 = __half22float2(*reinterpret_cast<const __half2*>(&sg[kc]));
+            const float2 s8 = __half22float2(*reinterpret_cast<const __half2*>(&sg8[kc]));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t h[4], h8[4];
+                widen_q4_key(r[2 * c], ex, h);
+                widen_q4_key(r[2 * c + 1], ex, h8);
+                const uint32_t a0[4] = {h[0], h8[0], h[1], h8[1]}, a1[4] = {h[2], h8[2], h[3], h8[3]};
+                const int grp = 2 * kc + c;
+                const float f0 = c ? s0.y : s0.x, f8 = c ? s8.y : s8.x;
+#pragma unroll
+                for (int nt = 0; nt < NTW; ++nt) {
+                    float acc[4];
+                    ptx::mma_f16_from(acc, a0, q[nt][2 * grp][0], q[nt][2 * grp][1], bias[nt][grp][0], bias[nt][grp][1]);
+                    ptx::mma_f16(acc, a1, q[nt][2 * grp + 1][0], q[nt][2 * grp + 1][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float f = e < 2 ? f0 : f8;
+                        x[nt][e] = grp == 0 ? f * acc[e] : fmaf(f, acc[e], x[nt][e]);
+                    }
+                }
+            }
+        }
+    }
+
+    if (GENERAL) {
+#pragma unroll
+        for (int nt = 0; nt < NTW; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float v = x[nt][e];
+                if (p.softcap_log2e > 0.f) v = tanhf(v) * p.softcap_log2e;
+                const int key = kbase + g + 8 * (e >> 1);
+                bool ok = key_ok(key, lo, hi);
+                if (causal)
+                    ok = ok && key <= kmax[nt][e & 1] && (key >= kmin[nt][e & 1] || (FIRST && key < p.first_tokens));
+                x[nt][e] = ok ? v : -INFINITY;
+            }
+    }
+
+    bool raise = false;
+#pragma unroll
+    for (int nt = 0; nt < NTW; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) raise |= fmaxf(x[nt][j], x[nt][j + 2]) > m[nt][j] + 8.f;
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < NTW; ++nt) {
+            float f[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float mx = fmaxf(m[nt][j], fmaxf(x[nt][j], x[nt][j + 2]));
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                f[j] = mx == -INFINITY ? 1.f : ptx::ex2(m[nt][j] - mx);
+                m[nt][j] = mx;
+                l[nt][j] *= f[j];
+            }
+#pragma unroll
+            for (int mi = 0; mi < D / 16; ++mi) {
+                o[nt][mi][0] *= f[0];
+                o[nt][mi][1] *= f[1];
+                o[nt][mi][2] *= f[0];
+                o[nt][mi][3] *= f[1];
+            }
+        }
+    }
+    uint32_t b[NTW][2];  // the weights as the B operand (keys x rows)
+#pragma unroll
+    for (int nt = 0; nt < NTW; ++nt) {
+        // without masked keys every row has a maximum by now
+        const float mu0 = GENERAL && m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+        const float mu1 = GENERAL && m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+        const float w0 = ptx::ex2(x[nt][0] - mu0), w1 = ptx::ex2(x[nt][1] - mu1);
+        const float w2 = ptx::ex2(x[nt][2] - mu0), w3 = ptx::ex2(x[nt][3] - mu1);
+        l[nt][0] += w0 + w2;
+        l[nt][1] += w1 + w3;
+        b[nt][0] = ptx::movmatrix_trans(pack_f16(w0, w1));
+        b[nt][1] = ptx::movmatrix_trans(pack_f16(w2, w3));
+    }
+
+    uint32_t w0[D / 64], w1[D / 64], w8[D / 64], w9[D / 64];  // scales of keys 2t, + 1, + 8, + 9
+    load_words<D / 64>(vsc, w0);
+    load_words<D / 64>(vsc + SH::kScaleRow, w1);
+    load_words<D / 64>(vsc + 8 * SH::kScaleRow, w8);
+    load_words<D / 64>(vsc + 9 * SH::kScaleRow, w9);
+    if (GENERAL) {  // a masked key's scales may be anything: zero
+        const int kq = kbase + 2 * t;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            if (!key_ok(kq, lo, hi)) w0[j] = 0u;
+            if (!key_ok(kq + 1, lo, hi)) w1[j] = 0u;
+            if (!key_ok(kq + 8, lo, hi)) w8[j] = 0u;
+            if (!key_ok(kq + 9, lo, hi)) w9[j] = 0u;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+        uint32_t r[4];
+        ptx::ldsm_x4_trans(r, vaddr ^ (32 * j));
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t h[4], h8[4];
+            widen_q4_value(r[c], __byte_perm(w0[j], w1[j], c ? 0x7632 : 0x5410), ex, h);
+            widen_q4_value(r[2 + c], __byte_perm(w8[j], w9[j], c ? 0x7632 : 0x5410), ex, h8);
+            const uint32_t a0[4] = {h[0], h[1], h8[0], h8[1]}, a1[4] = {h[2], h[3], h8[2], h8[3]};
+#pragma unroll
+            for (int nt = 0; nt < NTW; ++nt) {
+                ptx::mma_f16(o[nt][4 * j + 2 * c], a0, b[nt][0], b[nt][1]);
+                ptx::mma_f16(o[nt][4 * j + 2 * c + 1], a1, b[nt][0], b[nt][1]);
+            }
+        }
+    }
+}
+
 // FIRST: the launch keeps first tokens behind a window (PartialParams.first_tokens).
 // A template argument: as a run-time choice it cost the others 1 (bf16) to 6 %
 // (4-token chunks) in registers and mask instructions.
 template <int D, int KV, int NHT, bool FIRST>
-__global__ void __launch_bounds__(cta_threads(NHT), (D == 256 || NHT == 2 ? 1 : 2))
+__global__ void __launch_bounds__(Shape<D, KV, NHT>::kThreads, (Shape<D, KV, NHT>::kPerSM))
 partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_ks,
                   const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt,
@@ -806,14 +1034,15 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     constexpr int TK = SH::kTK;     // keys per stage
     constexpr int KS = D / 16;      // k-steps of QK, m-tiles of PV
     constexpr int HC = 8 * NHT;     // head columns of a unit
-    constexpr int CW = consumer_warps(NHT);          // consumer warps
-    constexpr int NTW = NHT * kKeyGroups / CW;       // 8-column tiles per consumer warp
+    constexpr int CW = SH::kConsumers;               // consumer warps
+    constexpr int NTW = SH::kTilesPerWarp;           // 8-column tiles per consumer warp
     constexpr int kProducerWarp = CW, kPrepWarp = CW + 1;
-    // merge scratch (inside one stage): all of D at once if it fits, else halves or quarters
+    // merge scratch (inside one stage): all of D at once if it fits, else halves, quarters or eighths
     constexpr int kScratchRow = 2 * kKeyGroups * HC * 4;
     constexpr int RC = kKeyGroups * HC * (D + 4) * 4 + kScratchRow <= SH::kStageBytes       ? D
                        : kKeyGroups * HC * (D / 2 + 4) * 4 + kScratchRow <= SH::kStageBytes ? D / 2
-                                                                                           : D / 4;
+                       : kKeyGroups * HC * (D / 4 + 4) * 4 + kScratchRow <= SH::kStageBytes ? D / 4
+                                                                                           : D / 8;
     static_assert(kKeyGroups * HC * (RC + 4) * 4 + kScratchRow <= SH::kStageBytes,
                   "merge scratch must fit in one stage");
     extern __shared__ uint8_t smem_raw[];
@@ -1028,6 +1257,7 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     prep_fused_q<D, HC, __nv_bfloat16, FRAG>(p, sg.b, h0, nh, rot, sg.b != cs_b, fits ? L : 0, freq_s,
                                                             cs_s, frag, SH::kFragRow, seg == 0 ? go : 0u, lane);
                 cs_b = sg.b;
+                if (Q4) q4_group_sums<D, HC>(frag, SH::kFragRow, lane);
                 // the q' fragments go to the consumers first; the new rows are needed only at
                 // the segment's last stage (rows_ready)
                 __syncwarp();
@@ -1047,6 +1277,7 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 continue;
             } else {
                 prep_loaded_q<D, HC, FRAG>(p, sg.b, sg.kvh, r0, nh, frag, SH::kFragRow, seg == 0 ? go : 0u, lane);
+                if (Q4) q4_group_sums<D, HC>(frag, SH::kFragRow, lane);
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar_qfull);
@@ -1072,6 +1303,12 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const float cap2 = p.softcap_log2e;
     // ldmatrix lane roles: matrix q = lane / 8, row r = lane % 8 of that matrix.
     const int lq = lane >> 3, lr = lane & 7;
+    // 4-bit caches: this lane's places in a stage (consume_q4)
+    const uint32_t q4_koff = Q4 ? code_off<D / 2, TK>(key_w + lr + 8 * (lq & 1), lq >> 1) : 0u;
+    const uint32_t q4_voff = Q4 ? SH::kKBytes + code_off<D / 2, TK>(key_w + lr + 8 * (lq >> 1), lq & 1) : 0u;
+    const Q4Exponents ex = q4_exponents(p);
+    const int q4_ksc = SH::kKScaleOff + (key_w + g) * SH::kScaleRow;
+    const int q4_vsc = SH::kVScaleOff + (key_w + 2 * t) * SH::kScaleRow;
     bool failed = false;
     int it = 0;   // stages consumed
     int seg = 0;  // segments consumed
@@ -1096,6 +1333,8 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 kmax[nt][j] = lens[sg.b] - p.q_len + tok;
                 kmin[nt][j] = p.attn_window > 0 ? kmax[nt][j] - p.attn_window + 1 : INT_MIN;
             }
+
+        const int all_hi = lens[sg.b] - p.q_len + 1, all_lo = p.attn_window > 0 ? lens[sg.b] - p.attn_window : 0;
 
         // fused append: the new key (slot L) is row new_r of the unit's last stage,
         // which consumer warp new_w owns; -1 when this segment does not end the unit
@@ -1139,6 +1378,20 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 }
             }
         }
+        // 4-bit keys: the accumulators' start, -72 times the sum of q' over each group
+        // (consume_q4) for columns 2t and 2t + 1
+        float bias[Q4 ? NTW : 1][Q4 ? D / 32 : 1][2];
+        if (Q4) {
+#pragma unroll
+            for (int nt = 0; nt < NTW; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float* row =
+                        reinterpret_cast<const float*>(frag + ((nt0 + nt) * 8 + 2 * t + j) * SH::kFragRow + 2 * D);
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) bias[nt][c][j] = row[c];
+                }
+        }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar_qempty);  // the slot may be refilled
 
@@ -1178,6 +1431,28 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             if (!failed && kbase < hi && kbase + 16 * MG > lo) {
                 const bool whole = kbase >= lo && kbase + 16 * MG <= hi;
                 const uint32_t st = base + s * SH::kStageBytes;
+                if constexpr (Q4) {
+                    // a group at a time, in a loop that is not unrolled: the body with its few taken
+                    // branches stays in the instruction cache
+                    const uint8_t* sp = base_ptr + s * SH::kStageBytes;
+                    // a chunk's rows all see the keys from all_lo up to the first token's, and the first tokens
+                    const bool all = !causal || (kbase >= all_lo && kbase + 16 * MG <= all_hi) || (FIRST && sg.st0 + k < sg.nf);
+                    if (whole && all && cap2 == 0.f) {
+#pragma unroll 1
+                        for (int mg = 0; mg < MG; ++mg)
+                            consume_q4<SH, NTW, FIRST, false>(
+                                p, st + q4_koff + 16 * mg * SH::kKRow, st + q4_voff + 16 * mg * SH::kVRow,
+                                sp + q4_ksc + 16 * mg * SH::kScaleRow, sp + q4_vsc + 16 * mg * SH::kScaleRow, 0, lo, hi,
+                                false, kmax, kmin, qhi, bias, ex, m, l, o, lane);
+                    } else {
+#pragma unroll 1
+                        for (int mg = 0; mg < MG; ++mg)
+                            consume_q4<SH, NTW, FIRST, true>(
+                                p, st + q4_koff + 16 * mg * SH::kKRow, st + q4_voff + 16 * mg * SH::kVRow,
+                                sp + q4_ksc + 16 * mg * SH::kScaleRow, sp + q4_vsc + 16 * mg * SH::kScaleRow,
+                                kbase + 16 * mg, lo, hi, causal, kmax, kmin, qhi, bias, ex, m, l, o, lane);
+                    }
+                } else {
 
                 // S^T = K . Q'^T (keys x heads), one accumulator per 16-key group
                 float sacc[MG][NTW][4];
@@ -1186,39 +1461,7 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                     for (int nt = 0; nt < NTW; ++nt)
                         sacc[mg][nt][0] = sacc[mg][nt][1] = sacc[mg][nt][2] = sacc[mg][nt][3] = 0.f;
-                if (Q4) {
-                    // 4-bit keys: one ldmatrix.x4 covers 16 keys x 64 dims (groups 2 kc and 2 kc + 1);
-                    // register j holds key g (+8 for odd j), dims 8t .. 8t + 7 of group 2 kc + j / 2,
-                    // widened to code * scale in fp16, exactly; the pairs (i, i + 4) of the 8 dims
-                    // are the operands of two k-steps
-                    const uint8_t* ksc = base_ptr + s * SH::kStageBytes + SH::kKScaleOff;
-#pragma unroll
-                    for (int mg = 0; mg < MG; ++mg) {
-                        uint32_t sg2[D / 64], sg8[D / 64];  // the scales of keys g and g + 8, two groups a word
-                        load_words<D / 64>(ksc + (key_w + 16 * mg + g) * SH::kScaleRow, sg2);
-                        load_words<D / 64>(ksc + (key_w + 16 * mg + g + 8) * SH::kScaleRow, sg8);
-#pragma unroll
-                        for (int kc = 0; kc < D / 64; ++kc) {
-                            uint32_t r[4];
-                            ptx::ldsm_x4(r, st + code_off<D / 2, TK>(key_w + 16 * mg + lr + 8 * (lq & 1), 2 * kc + (lq >> 1)));
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const uint32_t s0 = __byte_perm(sg2[kc], 0, c ? 0x3232 : 0x1010), m0 = neg24(s0);
-                                const uint32_t s8 = __byte_perm(sg8[kc], 0, c ? 0x3232 : 0x1010), m8 = neg24(s8);
-                                const uint32_t a0[4] = {widen_q4<0>(r[2 * c], s0, m0), widen_q4<0>(r[2 * c + 1], s8, m8),
-                                                        widen_q4<1>(r[2 * c], s0, m0), widen_q4<1>(r[2 * c + 1], s8, m8)};
-                                const uint32_t a1[4] = {widen_q4<2>(r[2 * c], s0, m0), widen_q4<2>(r[2 * c + 1], s8, m8),
-                                                        widen_q4<3>(r[2 * c], s0, m0), widen_q4<3>(r[2 * c + 1], s8, m8)};
-                                const int kk = 2 * (2 * kc + c);
-#pragma unroll
-                                for (int nt = 0; nt < NTW; ++nt) {
-                                    ptx::mma_f16(sacc[mg][nt], a0, qhi[nt][kk][0], qhi[nt][kk][1]);
-                                    ptx::mma_f16(sacc[mg][nt], a1, qhi[nt][kk + 1][0], qhi[nt][kk + 1][1]);
-                                }
-                            }
-                        }
-                    }
-                } else if (KQ8) {
+                if (KQ8) {
                     // int8 keys: one ldmatrix.x4 covers 16 keys x 32 dims (k-steps 2 kc and
                     // 2 kc + 1); register j holds key g (+8 for odd j), dims 4t .. 4t + 3 of
                     // 16-byte chunk 2 kc + j / 2, widened exactly to fp16 pairs
@@ -1367,10 +1610,7 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                     for (int nt = 0; nt < NTW; ++nt) {
                         uint32_t h01, l01, h23, l23;
-                        if (Q4) {  // one fp16 part: 2^-12 relative, on a weight of at most 1
-                            h01 = pack_f16(x[mg][nt][0], x[mg][nt][1]);
-                            h23 = pack_f16(x[mg][nt][2], x[mg][nt][3]);
-                        } else if (VQ8) {
+                        if (VQ8) {
                             split_f16(x[mg][nt][0] * w_g[mg], x[mg][nt][1] * w_g[mg], h01, l01);     // key g
                             split_f16(x[mg][nt][2] * w_g8[mg], x[mg][nt][3] * w_g8[mg], h23, l23);   // key g+8
                         } else {
@@ -1379,54 +1619,11 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         }
                         bph[nt][0] = ptx::movmatrix_trans(h01);
                         bph[nt][1] = ptx::movmatrix_trans(h23);
-                        if (!Q4) {
-                            bpl[nt][0] = ptx::movmatrix_trans(l01);
-                            bpl[nt][1] = ptx::movmatrix_trans(l23);
-                        }
+                        bpl[nt][0] = ptx::movmatrix_trans(l01);
+                        bpl[nt][1] = ptx::movmatrix_trans(l23);
                     }
                     const int krow = key_w + 16 * mg;  // this group's first row in the stage
-                    if (Q4) {
-                        // O^T += V^T . P^T from the 4-bit stage: ldmatrix.trans hands a lane the 4 dims
-                        // 32 c + 4 g .. + 3 (a b16 element) of keys 2t and 2t + 1; nibble i of both is the
-                        // fp16 pair of dim 4 g + i. m-tile 2 c has dims 4 g (row g) and 4 g + 1 (row
-                        // g + 8) of group c, m-tile 2 c + 1 dims 4 g + 2 and 4 g + 3.
-                        const uint32_t vst = st + SH::kKBytes;
-                        const uint8_t* vsc = base_ptr + s * SH::kStageBytes + SH::kVScaleOff;
-                        uint32_t w0[D / 64], w1[D / 64], w8[D / 64], w9[D / 64];  // scales of keys 2t, +1, +8, +9
-                        load_words<D / 64>(vsc + (krow + 2 * t) * SH::kScaleRow, w0);
-                        load_words<D / 64>(vsc + (krow + 2 * t + 1) * SH::kScaleRow, w1);
-                        load_words<D / 64>(vsc + (krow + 2 * t + 8) * SH::kScaleRow, w8);
-                        load_words<D / 64>(vsc + (krow + 2 * t + 9) * SH::kScaleRow, w9);
-                        if (!whole) {  // a masked key's scales may be anything: zero
-                            const int kq = kbase + 16 * mg + 2 * t;
-#pragma unroll
-                            for (int j = 0; j < D / 64; ++j) {
-                                if (!key_ok(kq, lo, hi)) w0[j] = 0u;
-                                if (!key_ok(kq + 1, lo, hi)) w1[j] = 0u;
-                                if (!key_ok(kq + 8, lo, hi)) w8[j] = 0u;
-                                if (!key_ok(kq + 9, lo, hi)) w9[j] = 0u;
-                            }
-                        }
-#pragma unroll
-                        for (int j = 0; j < D / 64; ++j) {
-                            uint32_t r[4];
-                            ptx::ldsm_x4_trans(r, vst + code_off<D / 2, TK>(krow + lr + 8 * (lq >> 1), 2 * j + (lq & 1)));
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const uint32_t s0 = __byte_perm(w0[j], w1[j], c ? 0x7632 : 0x5410), m0 = neg24(s0);
-                                const uint32_t s8 = __byte_perm(w8[j], w9[j], c ? 0x7632 : 0x5410), m8 = neg24(s8);
-                                const uint32_t a0[4] = {widen_q4<0>(r[c], s0, m0), widen_q4<1>(r[c], s0, m0),
-                                                        widen_q4<0>(r[2 + c], s8, m8), widen_q4<1>(r[2 + c], s8, m8)};
-                                const uint32_t a1[4] = {widen_q4<2>(r[c], s0, m0), widen_q4<3>(r[c], s0, m0),
-                                                        widen_q4<2>(r[2 + c], s8, m8), widen_q4<3>(r[2 + c], s8, m8)};
-#pragma unroll
-                                for (int nt = 0; nt < NTW; ++nt) {
-                                    ptx::mma_f16(o[nt][4 * j + 2 * c], a0, bph[nt][0], bph[nt][1]);
-                                    ptx::mma_f16(o[nt][4 * j + 2 * c + 1], a1, bph[nt][0], bph[nt][1]);
-                                }
-                            }
-                        }
-                    } else if (VQ8) {
+                    if (VQ8) {
                         // O^T += V^T . P^T straight from the int8 stage: one ldmatrix.x4.trans covers
                         // 16 keys x 32 values = m-tiles 2j (values 32j .. 32j+15) and 2j+1; in m-tile
                         // mi row g holds value 16 mi + 2g and row g + 8 holds 16 mi + 2g + 1.
@@ -1474,6 +1671,7 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                             }
                         }
                     }
+                }
                 }
             }
             if (k + 1 < sg.n_st) {  // the segment's last stage is held for the merge scratch
@@ -1580,7 +1778,7 @@ cudaError_t launch_one(const PartialParams& p, const PartialMaps& m, int n_ctas,
         if (e != cudaSuccess) return e;
         if (dev < 31) configured_device_mask |= 1 << dev;
     }
-    return launch_dependent(kern, dim3(n_ctas), dim3(cta_threads(NHT)), SH::kSmemBytes, s, m.k, m.v, m.s, m.ks, m.kt,
+    return launch_dependent(kern, dim3(n_ctas), dim3(SH::kThreads), SH::kSmemBytes, s, m.k, m.v, m.s, m.ks, m.kt,
                             m.vt, m.st, m.kst, p);
 }
 

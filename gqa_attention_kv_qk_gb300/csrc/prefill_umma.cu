@@ -1,7 +1,10 @@
 // prefill_umma.cu -- attention of a long chunk of tokens (a prefill chunk) over
 // a contiguous bf16 cache on the 5th-generation tensor cores (tcgen05): step 2
 // for steps of many tokens per sequence, after the separate append has written
-// the chunk's rows and q'.
+// the chunk's rows and q'. For a 4-bit cache the same over its visible rows
+// widened to fp16 in the workspace (cache_rows.cu; code * scale is an fp16
+// number): F16, where q' and P are one fp16 part each (2^-11 relative, against
+// keys and values of 4 bits) and half the MMAs are issued.
 //
 // The (token, head) rows of one kv head (token-major: row r is token r / G,
 // query head r % G of the group, as in query_row) are cut into blocks of 128.
@@ -98,8 +101,15 @@ __device__ __forceinline__ void um_split_trunc(float x0, float x1, uint32_t& hi,
     lo = __byte_perm(__float_as_uint(x0 - __uint_as_float(h0)), __float_as_uint(x1 - __uint_as_float(h1)), 0x7632);
 }
 
+__device__ __forceinline__ uint32_t um_pack_f16(float lo, float hi)
+{
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
 // FIRST: the launch keeps first tokens behind a window (PrefillParams.first_tokens).
-template <int D, bool FIRST>
+// F16: fp16 keys and values of row_cap rows per (sequence, kv head).
+template <int D, bool FIRST, bool F16>
 __global__ void __launch_bounds__(kUmThreads, 1)
 prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const PrefillParams p)
@@ -109,8 +119,11 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     constexpr int KS = D / 16;       // k-steps of Q'.K^T
     constexpr int KH = kUmKeys / kUmSplit;  // keys per softmax thread and block
     constexpr int CW = D / kUmSplit;        // O columns per softmax thread
-    constexpr uint32_t kIdS = ptx::umma_idesc_bf16(kUmRows, kUmKeys, false, false);
-    constexpr uint32_t kIdO = ptx::umma_idesc_bf16(kUmRows, D, false, true);
+    constexpr uint32_t kIdS = F16 ? ptx::umma_idesc_f16(kUmRows, kUmKeys, false, false)
+                                  : ptx::umma_idesc_bf16(kUmRows, kUmKeys, false, false);
+    constexpr uint32_t kIdO = F16 ? ptx::umma_idesc_f16(kUmRows, D, false, true)
+                                  : ptx::umma_idesc_bf16(kUmRows, D, false, true);
+    constexpr int kParts = F16 ? 1 : 2;  // operand parts of q' and P
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -169,7 +182,7 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     // past them); a sequence the append could not take keeps its length and gets zero rows.
     const int L_after = p.seq_lens[b];
     const int L = L_after - p.q_len;
-    const bool valid = L >= 0 && L_after <= p.cap;
+    const bool valid = L >= 0 && L_after <= p.cap && (!F16 || L_after <= p.row_cap);
     const int r_first = rb * kUmRows, r_last = min(rows, r_first + kUmRows) - 1;
     // keys the block sees: [0, first) and [lo, hi) (Keys), in n_f and n_st - n_f key
     // blocks; block j starts at key block_key(j) and its keys lie in the run of its part
@@ -192,7 +205,7 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const uint32_t ring = is_v ? vring : kring;
             const uint32_t full = is_v ? bar_vfull : bar_kfull, empty = is_v ? bar_vempty : bar_kempty;
             const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
-            const int row0 = (b * p.Hkv + kvh) * p.cap;
+            const int row0 = (b * p.Hkv + kvh) * (F16 ? p.row_cap : p.cap);
             int issued = 0;
             for (int i = 0; i < n_st; ++i) {
                 const int s = i % NSL;
@@ -231,7 +244,7 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
-                    for (int part = 0; part < 2; ++part) {
+                    for (int part = 0; part < kParts; ++part) {
                         const uint32_t koff = (kk >> 2) * (kUmKeys * 128) + (kk & 3) * 32;
                         ptx::umma_bf16_ts(tmem, tmem + kUmQCol + part * (D / 2) + kk * 8,
                                           ptx::umma_desc(kt + koff, 16, 1024), kIdS, part | kk);
@@ -259,7 +272,7 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
                 for (int k2 = 0; k2 < kUmKeys / 16; ++k2)
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < kParts; ++part)
                         ptx::umma_bf16_ts(t_o, tmem + kUmPCol + part * (kUmKeys / 2) + k2 * 8,
                                           ptx::umma_desc(vt + k2 * 2048, kUmKeys * 128, 1024), kIdO,
                                           (j > 0 || part > 0 || k2 > 0) ? 1u : 0u);
@@ -300,11 +313,16 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 for (int e = 0; e < 4; ++e) {
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (row_ok) v = *reinterpret_cast<const float4*>(q + d0 + 4 * e);
-                    um_split(v.x, v.y, hh[2 * e], ll[2 * e]);
-                    um_split(v.z, v.w, hh[2 * e + 1], ll[2 * e + 1]);
+                    if (F16) {
+                        hh[2 * e] = um_pack_f16(v.x, v.y);
+                        hh[2 * e + 1] = um_pack_f16(v.z, v.w);
+                    } else {
+                        um_split(v.x, v.y, hh[2 * e], ll[2 * e]);
+                        um_split(v.z, v.w, hh[2 * e + 1], ll[2 * e + 1]);
+                    }
                 }
                 ptx::tmem_st8(tmem + lane_addr + kUmQCol + d0 / 2, hh);
-                ptx::tmem_st8(tmem + lane_addr + kUmQCol + D / 2 + d0 / 2, ll);
+                if (!F16) ptx::tmem_st8(tmem + lane_addr + kUmQCol + D / 2 + d0 / 2, ll);
             }
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
@@ -431,10 +449,15 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (ok) {
                 uint32_t hh[16], lw[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) um_split_trunc(x[2 * e], x[2 * e + 1], hh[e], lw[e]);
+                for (int e = 0; e < 16; ++e) {
+                    if (F16)
+                        hh[e] = um_pack_f16(x[2 * e], x[2 * e + 1]);
+                    else
+                        um_split_trunc(x[2 * e], x[2 * e + 1], hh[e], lw[e]);
+                }
                 const uint32_t tp = tmem + lane_addr + kUmPCol + (KH / 2) * h;
                 ptx::tmem_st16(tp, hh);
-                ptx::tmem_st16(tp + kUmKeys / 2, lw);
+                if (!F16) ptx::tmem_st16(tp + kUmKeys / 2, lw);
                 ptx::tmem_wait_st();
             }
             ptx::tc_fence_before();
@@ -507,12 +530,12 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     }
 }
 
-template <int D, bool FIRST>
+template <int D, bool FIRST, bool F16>
 cudaError_t launch_um(const PrefillParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s)
 {
     using SH = UmShape<D>;
     static_assert(SH::kSmemBytes <= 232448, "shared memory of the prefill kernel");
-    auto kern = prefill_umma_kernel<D, FIRST>;
+    auto kern = prefill_umma_kernel<D, FIRST, F16>;
     static int configured_device_mask = 0;  // bit per device that has the smem attribute set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -529,13 +552,21 @@ cudaError_t launch_um(const PrefillParams& p, const CUtensorMap& tk, const CUten
     return launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), dim3(kUmThreads), SH::kSmemBytes, s, tk, tv, p);
 }
 
+template <int D>
+cudaError_t launch_d(const PrefillParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s)
+{
+    const bool f16 = p.row_cap > 0;
+    if (p.first_tokens > 0) return f16 ? launch_um<D, true, true>(p, tk, tv, s) : launch_um<D, true, false>(p, tk, tv, s);
+    return f16 ? launch_um<D, false, true>(p, tk, tv, s) : launch_um<D, false, false>(p, tk, tv, s);
+}
+
 }  // namespace
 
 cudaError_t launch_prefill_umma(const PrefillParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s)
 {
     switch (p.D) {
-    case 64: return p.first_tokens > 0 ? launch_um<64, true>(p, tk, tv, s) : launch_um<64, false>(p, tk, tv, s);
-    case 128: return p.first_tokens > 0 ? launch_um<128, true>(p, tk, tv, s) : launch_um<128, false>(p, tk, tv, s);
+    case 64: return launch_d<64>(p, tk, tv, s);
+    case 128: return launch_d<128>(p, tk, tv, s);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -240,14 +240,15 @@ typedef struct {
 /* Where each array lives in the workspace, and the split geometry. */
 typedef struct {
     int32_t n_ctas;           /* P: persistent CTAs of the partial step (stream-K ranges) */
-    int32_t stage_keys;       /* keys per ring stage: 64; 128 for q8 and q4 at head_dim 128 / 256;
-                                 at head_dim 64 128 (bf16), 256 (vq8, q8, q4) */
+    int32_t stage_keys;       /* keys per ring stage: 64; 128 for q8 at head_dim 128 / 256 and q4 at 256;
+                                 at head_dim 64 128 (bf16), 256 (vq8, q8);
+                                 256 for q4 at head_dim 64 / 128 */
     int32_t heads_per_cta;    /* query rows (token, head) of one unit (sequence, kv head, row group) */
     int32_t kernel;           /* 0: fp32 CUDA-core partial, 1: TMA + tensor-core partial,
-                                 2: query-tiled prefill on a contiguous cache (bf16 cache,
-                                 head_dim 64 / 128, q_len x G >= 128 rows per kv head;
-                                 a paged cache of this geometry takes kernel 1, whose
-                                 fields the others still describe) */
+                                 2: query-tiled prefill (bf16 and 4-bit caches, head_dim
+                                 64 / 128, q_len x G >= 128 rows per kv head; a paged bf16
+                                 cache of this geometry takes kernel 1, whose fields the
+                                 others still describe) */
     int32_t n_slices;         /* partial + combine launches (batch slices) */
     int32_t slice_batch;      /* sequences per slice (the last may hold fewer) */
     int32_t step_kernels;     /* kernels one uaa_decode_attn call launches (contiguous cache) */
@@ -290,7 +291,11 @@ uaa_status uaa_rope_qk_norm_append(const uaa_attn_desc* desc, const uaa_step_arg
  * query-tiled prefill kernel instead: a CTA per (sequence, kv head, block of
  * 128 rows) reads each key and value tile its rows see once, and writes the
  * block's output rows itself (sink included); rows of a sequence the append
- * could not take are zero. Step 3 then has nothing to do. */
+ * could not take are zero. Step 3 then has nothing to do. A 4-bit cache, paged or
+ * not, takes it too, over its visible rows widened to fp16 in the workspace (up to
+ * 512 MiB of it, some sequences at a time); there a sequence beyond
+ * max_seq_len (UAA_DEVFLAG_LEN_HINT) has no room in the workspace and gets zero
+ * rows. */
 uaa_status uaa_decode_attn_partial(const uaa_attn_desc* desc, const uaa_step_args* args,
                                    const uaa_workspace* ws, cudaStream_t stream);
 

@@ -75,7 +75,7 @@ def test_read_refusals():
 
 
 def test_geometry():
-    for D, keys, per_sm in ((64, 256, 2), (128, 128, 2), (256, 128, 1)):
+    for D, keys, per_sm in ((64, 256, 2), (128, 256, 2), (256, 128, 1)):
         lay = B.uaa_get_workspace_layout(B.make_desc(config(head_dim=D)), 4, 100, 152)
         assert (lay.kernel, lay.stage_keys, lay.n_ctas) == (1, keys, 152 * per_sm)
 
@@ -153,6 +153,13 @@ CASES = {
     "paged32-d64-window": (dict(head_dim=64, window=37), [500, 20], 1, 32),
     "paged256-first": (dict(window=300, first_tokens=40), [1500, 340, 341], 1, 256),
     "paged64-chunk9-d256": (dict(head_dim=256), [300, 60], 9, 64),
+    # 128 (token, head) rows and more per kv head: widened rows and the prefill kernel
+    "prefill-window-sink": (dict(window=100, has_sink=True), [500, 0, 127], 40, 0),
+    "prefill-first": (dict(window=150, first_tokens=100), [700, 250, 251, 252, 20], 33, 0),
+    "prefill-d64-first-softcap": (dict(window=128, first_tokens=200, head_dim=64, softcap=20.0), [900, 328, 327], 64, 0),
+    "prefill-paged32": (dict(), [300, 31, 0], 70, 32),
+    "prefill-paged256-first-bf16": (dict(window=300, first_tokens=40, out_dtype="bf16"), [1500, 340, 341], 64, 256),
+    "prefill-norm-interleaved": (dict(qk_norm=True, norm_w_range=(0.5, 1.5), rope_style="interleaved"), [130], 50, 0),
 }
 
 
@@ -237,6 +244,47 @@ def test_step(name, entry):
         err = (err - want.abs() * torch.finfo(torch.bfloat16).eps / 2).clamp(min=0)
     assert float(err.max()) <= TOL_MAX, float(err.max())
     assert float(err.mean()) <= TOL_MEAN, float(err.mean())
+
+
+@pytest.mark.gpu
+def test_prefill_in_batch_slices():
+    """More widened rows than the workspace holds at once: the sequences go through it
+    some at a time, and give what each gives alone."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    lens, T = [30, 0, 200, 64, 127, 128, 129, 1, 77], 40
+    cfg = config(n_q_heads=32, n_kv_heads=8, batch=len(lens), seq_len=max(lens), q_len=T)
+    lay = B.uaa_get_workspace_layout(B.make_desc(cfg), len(lens), 16000, 0, T)
+    assert lay.kernel == 2 and lay.step_kernels == 1 + 2 * 2
+    case = W.host_case(cfg, lens=lens)
+    one = DecodeLayer.for_case(case)
+    big = DecodeLayer(cfg, len(lens), 16000 + 64, max_q_len=T)
+    for n in ("k_cache", "v_cache", "k_scale", "v_scale"):
+        getattr(big, n)[:, :, :case["cap"]] = getattr(one, n)
+    big.seq_lens.copy_(one.seq_lens)
+    dev = {k: case[k].cuda() for k in ("q", "k_new", "v_new")}
+    want = one.step(dev["q"], dev["k_new"], dev["v_new"]).clone()
+    got = big.step(dev["q"], dev["k_new"], dev["v_new"], max_seq_len=16000)
+    torch.cuda.synchronize()
+    assert one.device_status() == 0 and big.device_status() == 0
+    assert torch.equal(got, want)
+
+
+@pytest.mark.gpu
+def test_prefill_beyond_the_length_bound():
+    """A sequence longer than max_seq_len has no room for its widened rows: flagged, its
+    rows are zero, the others as they are."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    lens, T = [500, 30], 64
+    cfg = config(batch=2, seq_len=500, q_len=T)
+    case = W.host_case(cfg, lens=lens)
+    a, b = DecodeLayer.for_case(case), DecodeLayer.for_case(case)
+    dev = {k: case[k].cuda() for k in ("q", "k_new", "v_new")}
+    want = a.step(dev["q"], dev["k_new"], dev["v_new"]).clone()
+    got = b.step(dev["q"], dev["k_new"], dev["v_new"], max_seq_len=100)
+    torch.cuda.synchronize()
+    assert a.device_status() == 0 and b.device_status() == B.UAA_DEVFLAG_LEN_HINT
+    assert torch.equal(got[1], want[1]) and not got[0].any()
+    assert torch.equal(a.k_cache, b.k_cache) and torch.equal(a.seq_lens, b.seq_lens)
 
 
 @pytest.mark.gpu
