@@ -180,12 +180,19 @@ __global__ void __launch_bounds__(kRowThreads) widen_q4_kernel(const WidenParams
         } else if (seen && e == 0) {
             atomicOr(p.status, UAA_DEVFLAG_PAGE);
         }
+        // byte j (codes 2 j and 2 j + 1) in both halves of a word; the low nibble of the
+        // lower half as 1024 + u, the high nibble of the upper one as 64 + u, less 1032 and
+        // 72: the codes, exactly; times the scale (3 bits times 8), exactly
+        const uint32_t exponents = 0x54006400u + (static_cast<uint32_t>(p.D) >> 16);  // not a literal: one and-or
+        const __half2 off = __halves2half2(__float2half_rn(1032.f), __float2half_rn(72.f));
         uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t u = ((j < 4 ? c.x : c.y) >> (8 * (j & 3))) & 0xffu;
-            const __half2 v = __floats2half2_rn(static_cast<float>(u & 15u) - 8.f, static_cast<float>(u >> 4) - 8.f);
-            const __half2 x = __hmul2(v, s);  // exact: 3 bits times 8
+            const uint32_t u = __byte_perm(j < 4 ? c.x : c.y, 0, 0x0101 * (j & 3) | 0x4040);
+            const uint32_t t = (u & 0x00F0000Fu) | exponents;
+            __half2 v;
+            memcpy(&v, &t, 4);
+            const __half2 x = __hmul2(__hsub2(v, off), s);
             memcpy(&w[j], &x, 4);
         }
         uint4* o = reinterpret_cast<uint4*>(out + static_cast<size_t>(r) * p.D + 16 * e);

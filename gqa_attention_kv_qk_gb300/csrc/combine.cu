@@ -28,12 +28,15 @@ namespace {
 
 constexpr int kCombineMinThreads = 128;
 constexpr int kCombineMaxThreads = 512;
-constexpr int kMaxHeads = 16;    // heads of one unit
 constexpr int kRecBatch = 4;     // records loaded together per output element
 
+// D, HC (query rows per unit: 8 or 16) are template arguments: divisions by them at
+// run time were most of the code, and a kernel of a few microseconds that runs cold
+// pays for every line of it (5 us for a one-sequence step's combine, of 14).
+template <int D, int HC>
 __global__ void __launch_bounds__(kCombineMaxThreads) combine_kernel(const CombineParams p)
 {
-    extern __shared__ float wts[];  // [R][nh]: record log2-sum-exp, then weights
+    extern __shared__ float wts[];  // [R][HC]: record log2-sum-exp, then weights
     grid_dependency_wait();         // the partial kernel's records are complete
     allow_dependent_launch();
     if (blockIdx.x == gridDim.x - 1) {     // the extra CTA: the partial kernel's range balance
@@ -41,112 +44,129 @@ __global__ void __launch_bounds__(kCombineMaxThreads) combine_kernel(const Combi
         return;
     }
 
+    // the unit's first and last owner, left by the partial kernel (cleared for the next launch)
+    unsigned* own = p.owners + 2 * static_cast<size_t>(blockIdx.x);
+    const uint2 fl = *reinterpret_cast<const uint2*>(own);
+    const unsigned first = fl.x, last = fl.y;
     const int units = p.Hkv * p.head_groups;
     const int b = blockIdx.x / units, u = blockIdx.x - b * units;
     const int kvh = u / p.head_groups, hg = u - kvh * p.head_groups;
-    const int HC = p.heads_per_cta;
     const int r0 = hg * HC;                      // the unit's first query row (query_row)
     const int nh = min(HC, p.q_len * p.G - r0);  // its query rows
-    const int D = p.D;
     const int tid = threadIdx.x, nthr = blockDim.x;
-    // output element idx (row idx / D, column idx % D) of the unit
-    auto out_at = [&](int idx) {
-        const int hc = idx / D;
-        return query_row(b, r0 + hc, kvh, p.G, p.Hq, p.q_len) * D + (idx - hc * D);
-    };
-    // the unit's first and last owner, left by the partial kernel (cleared for the next launch)
-    unsigned* own = p.owners + 2 * static_cast<size_t>(blockIdx.x);
-    const unsigned first = own[0], last = own[1];
     __syncthreads();  // every thread has read the pair
-    if (tid == 0) {
-        own[0] = 0u;
-        own[1] = 0u;
-    }
-    if (first == 0u || last == 0u) {  // no visible key: zeros
-        for (int idx = tid; idx < nh * D; idx += nthr) store_out(p.out, p.out_dtype, out_at(idx), 0.f);
-        return;
-    }
+    if (tid == 0) *reinterpret_cast<uint2*>(own) = make_uint2(0u, 0u);
     const int cA = static_cast<int>(first & 0x7fffffffu) - 1, cB = static_cast<int>(last) - 1;
-    if (cA == cB) return;  // a whole unit: the partial kernel wrote it
-    if (cA < 0 || cB < cA || cB >= p.P) {  // owner words no range of this launch wrote: not read further
+    const bool empty = first == 0u || last == 0u;  // no visible key: zeros
+    if (!empty && cA == cB) return;                // a whole unit: the partial kernel wrote it
+    if (!empty && (cA < 0 || cB < cA || cB >= p.P)) {  // owner words no range of this launch wrote: not read further
         if (tid == 0) atomicOr(p.status, UAA_DEVFLAG_TIMEOUT);
         return;
     }
     const bool first_is_slot0 = (first & 0x80000000u) != 0u;
-    const int R = cB - cA + 1;  // the unit's records: owners cA .. cB
+    const int R = empty ? 0 : cB - cA + 1;  // the unit's records: owners cA .. cB
 
-    for (int i = tid; i < R * nh; i += nthr)
-        wts[i] = p.rec_lse[static_cast<size_t>(record_of(cA + i / nh, cA, first_is_slot0)) * HC + (i % nh)];
+    for (int i = tid; i < R * HC; i += nthr)
+        if (i % HC < nh) wts[i] = p.rec_lse[static_cast<size_t>(record_of(cA + i / HC, cA, first_is_slot0)) * HC + i % HC];
     __syncthreads();
-    for (int hc = tid; hc < nh; hc += nthr) {
+    for (int hc = tid; hc < nh && !empty; hc += nthr) {
         const float z = p.sink ? p.sink[kvh * p.G + (r0 + hc) % p.G] * kLog2e : -INFINITY;
         float M = z;
-        for (int r = 0; r < R; ++r) M = fmaxf(M, wts[r * nh + hc]);
+#pragma unroll 4
+        for (int r = 0; r < R; ++r) M = fmaxf(M, wts[r * HC + hc]);
         float den = 0.f;
         if (M != -INFINITY) {
             den = p.sink ? exp2f(z - M) : 0.f;
+#pragma unroll 1
             for (int r = 0; r < R; ++r) {
-                const float e = wts[r * nh + hc];
+                const float e = wts[r * HC + hc];
                 const float w = e == -INFINITY ? 0.f : exp2f(e - M);
-                wts[r * nh + hc] = w;
+                wts[r * HC + hc] = w;
                 den += w;
             }
         }
         const float inv = den > 0.f ? 1.f / den : 0.f;
-        for (int r = 0; r < R; ++r) wts[r * nh + hc] = M == -INFINITY ? 0.f : wts[r * nh + hc] * inv;
+#pragma unroll 1
+        for (int r = 0; r < R; ++r) wts[r * HC + hc] = M == -INFINITY ? 0.f : wts[r * HC + hc] * inv;
     }
     __syncthreads();
-    for (int base = tid; base < nh * D; base += 4 * nthr) {
+    // four neighbouring elements of a row per thread
+#pragma unroll 1
+    for (int i = tid; i < nh * (D / 4); i += nthr) {
+        const int hc = i / (D / 4), d = 4 * (i % (D / 4));
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int r0 = 0; r0 < R; r0 += kRecBatch) {
-            float v[kRecBatch][4];
+#pragma unroll 1
+        for (int r1 = 0; r1 < R; r1 += kRecBatch) {
+            float4 v[kRecBatch];
 #pragma unroll
-            for (int r = 0; r < kRecBatch; ++r)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int idx = base + k * nthr;
-                    v[r][k] = 0.f;
-                    if (r0 + r < R && idx < nh * D) {
-                        const int hc = idx / D, d = idx - hc * D;
-                        const int rec = record_of(cA + r0 + r, cA, first_is_slot0);
-                        v[r][k] = p.rec_o[(static_cast<size_t>(rec) * HC + hc) * D + d];
-                    }
+            for (int r = 0; r < kRecBatch; ++r) {
+                v[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r1 + r < R) {
+                    const int rec = record_of(cA + r1 + r, cA, first_is_slot0);
+                    v[r] = *reinterpret_cast<const float4*>(p.rec_o + (static_cast<size_t>(rec) * HC + hc) * D + d);
                 }
+            }
 #pragma unroll
             for (int r = 0; r < kRecBatch; ++r)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int idx = base + k * nthr;
-                    if (r0 + r < R && idx < nh * D) acc[k] = fmaf(wts[(r0 + r) * nh + idx / D], v[r][k], acc[k]);
+                if (r1 + r < R) {
+                    const float w = wts[(r1 + r) * HC + hc];
+                    acc[0] = fmaf(w, v[r].x, acc[0]);
+                    acc[1] = fmaf(w, v[r].y, acc[1]);
+                    acc[2] = fmaf(w, v[r].z, acc[2]);
+                    acc[3] = fmaf(w, v[r].w, acc[3]);
                 }
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int idx = base + k * nthr;
-            if (idx < nh * D) store_out(p.out, p.out_dtype, out_at(idx), acc[k]);
+        const size_t at = query_row(b, r0 + hc, kvh, p.G, p.Hq, p.q_len) * D + d;
+        if (p.out_dtype == UAA_DTYPE_F32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[0], acc[1]), hi = __floats2bfloat162_rn(acc[2], acc[3]);
+            uint2 w;
+            memcpy(&w.x, &lo, 4);
+            memcpy(&w.y, &hi, 4);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) = w;
         }
     }
+}
+
+template <int D, int HC>
+cudaError_t launch_combine_of(const CombineParams& p, cudaStream_t s)
+{
+    // one CTA per unit, and one that rebalances the partial kernel's ranges; a
+    // thread per four output elements of a unit's rows, in whole warps
+    const long long blocks = static_cast<long long>(p.B) * p.Hkv * p.head_groups + 1;
+    if (blocks == 1) return cudaSuccess;
+    const int rows = HC < p.q_len * p.G ? HC : p.q_len * p.G;
+    int threads = (rows * D / 4 + 31) / 32 * 32;
+    threads = threads < kCombineMinThreads ? kCombineMinThreads : (threads > kCombineMaxThreads ? kCombineMaxThreads : threads);
+    // weights for up to every range's record of a unit
+    const size_t smem = static_cast<size_t>(p.P) * HC * 4;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(combine_kernel<D, HC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
+    return launch_dependent(combine_kernel<D, HC>, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t s)
 {
-    // one CTA per unit, and one that rebalances the partial kernel's ranges; a
-    // thread per four output elements of a unit's rows, in whole warps
-    const long long blocks = static_cast<long long>(p.B) * p.Hkv * p.head_groups + 1;
-    if (blocks == 1) return cudaSuccess;
-    const int rows = p.heads_per_cta < p.q_len * p.G ? p.heads_per_cta : p.q_len * p.G;
-    int threads = (rows * p.D / 4 + 31) / 32 * 32;
-    threads = threads < kCombineMinThreads ? kCombineMinThreads : (threads > kCombineMaxThreads ? kCombineMaxThreads : threads);
-    // weights for up to every range's record of a unit
-    const size_t smem = static_cast<size_t>(p.P) * (p.heads_per_cta < kMaxHeads ? p.heads_per_cta : kMaxHeads) * 4;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(combine_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
+    if (p.heads_per_cta == 8) {
+        switch (p.D) {
+        case 64: return launch_combine_of<64, 8>(p, s);
+        case 128: return launch_combine_of<128, 8>(p, s);
+        case 256: return launch_combine_of<256, 8>(p, s);
+        default: return cudaErrorInvalidValue;
+        }
     }
-    return launch_dependent(combine_kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, s, p);
+    if (p.heads_per_cta != 16) return cudaErrorInvalidValue;
+    switch (p.D) {
+    case 64: return launch_combine_of<64, 16>(p, s);
+    case 128: return launch_combine_of<128, 16>(p, s);
+    default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace uaa

@@ -72,8 +72,8 @@ struct UmShape {
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kKSlots * kTile;
     static constexpr int kOffBar = kOffV + kVSlots * kTile;  // barriers and the TMEM address: 512 bytes
-    static constexpr int kOffXch = kOffBar + 512;             // the row exchange: [kUmSplit][128] floats
-    static constexpr int kSmemBytes = 1024 + kOffXch + kUmSplit * 4 * kUmRows;
+    static constexpr int kOffXch = kOffBar + 512;             // the row exchange: [2][kUmSplit][128] floats
+    static constexpr int kSmemBytes = 1024 + kOffXch + 2 * kUmSplit * 4 * kUmRows;
     static_assert(16 * (kKSlots + kVSlots) + 64 <= 512, "barrier area");
 };
 
@@ -124,6 +124,7 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     constexpr uint32_t kIdO = F16 ? ptx::umma_idesc_f16(kUmRows, D, false, true)
                                   : ptx::umma_idesc_bf16(kUmRows, D, false, true);
     constexpr int kParts = F16 ? 1 : 2;  // operand parts of q' and P
+    constexpr bool kTwoBuffers = F16 || FIRST;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -139,7 +140,7 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const uint32_t bar_drain = bar_pv + 8;       // every MMA done (MMA commit)
     const uint32_t tmem_slot = bar_drain + 8;
     uint32_t* tmem_slot_ptr = reinterpret_cast<uint32_t*>(smem_raw + (tmem_slot - raw));
-    float* xch = reinterpret_cast<float*>(smem_raw + (base + SH::kOffXch - raw));  // [kUmSplit][128]: row maxima / sums
+    float* xch = reinterpret_cast<float*>(smem_raw + (base + SH::kOffXch - raw));  // [2][kUmSplit][128]: row maxima / sums
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.q_len * p.G;  // query rows of the kv head
@@ -382,14 +383,16 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 for (int a = 0; a < 4; ++a) t8[a] = fmaxf(t8[a], t8[a + 4]);
                 mh = fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3]));
             }
-            // the row's maximum over its quarters (the second barrier: all have read
-            // before any writes again)
-            xch[h * kUmRows + r] = mh;
+            // the row's maximum over its quarters, through two buffers in turn: a warp that
+            // writes block j + 2's has passed block j + 1's barrier, so all have read block
+            // j's. (With bf16 parts one buffer and a second barrier ran 0.5 % faster.)
+            float* xb = xch + (kTwoBuffers ? (j & 1) * (kUmSplit * kUmRows) : 0);
+            xb[h * kUmRows + r] = mh;
             ptx::named_barrier_sync(quad_bar, 32 * kUmSplit);
             float mx = mh;
 #pragma unroll
-            for (int o = 1; o < kUmSplit; ++o) mx = fmaxf(mx, xch[((h + o) % kUmSplit) * kUmRows + r]);
-            ptx::named_barrier_sync(quad_bar, 32 * kUmSplit);
+            for (int o = 1; o < kUmSplit; ++o) mx = fmaxf(mx, xb[((h + o) % kUmSplit) * kUmRows + r]);
+            if (!kTwoBuffers) ptx::named_barrier_sync(quad_bar, 32 * kUmSplit);
 
             // raise the reference maximum where a logit exceeds it by more than 2^8
             const bool raise = mx > m + 8.f;
@@ -466,11 +469,12 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         if (!ok && lane == 0) atomicOr(p.status, UAA_DEVFLAG_TIMEOUT);
 
         // ------------------------------------------------------------ the rows
-        // the row's sum over its quarters
-        xch[h * kUmRows + r] = l;
+        // the row's sum over its quarters (the buffer after the last block's)
+        float* xb = xch + (kTwoBuffers ? (n_st & 1) * (kUmSplit * kUmRows) : 0);
+        xb[h * kUmRows + r] = l;
         ptx::named_barrier_sync(quad_bar, 32 * kUmSplit);
 #pragma unroll
-        for (int o = 1; o < kUmSplit; ++o) l += xch[((h + o) % kUmSplit) * kUmRows + r];
+        for (int o = 1; o < kUmSplit; ++o) l += xb[((h + o) % kUmSplit) * kUmRows + r];
         // O is complete once the last P . V has (commits complete in order)
         if (n_st > 0) {
             ok = __all_sync(0xffffffffu, ok && ptx::mbar_wait(bar_pv, (n_st - 1) & 1, kWaitLimitCycles));
