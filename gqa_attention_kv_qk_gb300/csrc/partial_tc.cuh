@@ -1134,77 +1134,92 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 
     if (warp == kProducerWarp) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            bool ok = true;
-            bool counted = false;  // fused: this CTA has counted in
-            int it = 0;            // stages issued
-            const uint64_t stream_policy = ptx::l2_evict_first_policy();  // keys and values are read once
+        // Lane 0 walks the stages and issues their loads. Paged caches: a lane per
+        // page-aligned sub-tile, which looks its page up (before the wait for a free
+        // stage) and issues its loads; a lane looking up one after the other waited
+        // for a memory round trip each.
+        static_assert(TK / 16 <= 32, "a lane per 16-key sub-tile");
+        const bool paged = p.pages.table != nullptr;
+        bool ok = true;
+        bool counted = false;  // fused: this CTA has counted in
+        int it = 0;            // stages issued
+        const uint64_t stream_policy = ptx::l2_evict_first_policy();  // keys and values are read once
+        if (lane == 0 || paged) {
             for (long long pos = s_c; pos < e_c && ok;) {
                 const Segment sg = segment_at(prefix, lens, p.B, p.window, FIRST ? p.first_tokens : 0, p.cap, MG, p.head_groups,
                                               units, pos, e_c,
                                               p.fused != 0);
                 const int head_row = (p.b_off + sg.b) * p.Hkv + sg.kvh;
-                const int row0 = p.pages.table ? 0 : head_row * p.cap;  // contiguous caches
+                const int row0 = paged ? 0 : head_row * p.cap;  // contiguous caches
                 const int t0 = sg.keys.lo / kTileKeys;
                 for (int k = 0; k < sg.n_st; ++k, ++it) {
                     const int s = it % SH::kStages;
-                    if (it == 1 && !ptx::flag_wait(go, kWaitLimitCycles)) {
-                        // the first stage is on its way; the rest of the ring follows the prep
-                        // warp's first q reads (release_producer)
-                        atomicOr(p.status, UAA_DEVFLAG_TIMEOUT);
-                        ok = false;
-                        break;
-                    }
-                    if (p.fused && !counted && it == SH::kStages) {  // the ring is full: wait time
-                        count_in_and_advance(p, lens);
-                        counted = true;
-                    }
-                    if (it >= SH::kStages &&
-                        !ptx::mbar_wait(bar_empty + 8 * s, ((it / SH::kStages) & 1) ^ 1, kWaitLimitCycles)) {
-                        atomicOr(p.status, UAA_DEVFLAG_TIMEOUT);
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t st = base + s * SH::kStageBytes;
-                    const uint32_t bar = bar_full + 8 * s;
                     const StageKeys sk = stage_keys<FIRST>(sg.keys, t0, sg.nf, sg.st0 + k, MG);
                     const int key = sk.key0;
+                    // paged: this lane's sub-tile of min(64, page_size) keys, if any of them is
+                    // visible (the others' rows of the stage are left as they are: masked by the
+                    // consumers). An entry that is no page reads as zeros from a negative row.
+                    const int sub = min(1 << p.pages.shift, kTileKeys);
+                    const int ku = key + lane * sub;
+                    const bool mine = paged && lane * sub < TK && ku < sk.hi && ku + sub > sk.lo;
+                    long long row = -1;
+                    if (mine) {
+                        row = cache_row(p.pages, p.Hkv, p.cap, p.b_off + sg.b, sg.kvh, ku);
+                        if (row < 0) atomicOr(p.status, UAA_DEVFLAG_PAGE);
+                    }
+                    if (lane == 0) {
+                        if (it == 1 && !ptx::flag_wait(go, kWaitLimitCycles)) {
+                            // the first stage is on its way; the rest of the ring follows the prep
+                            // warp's first q reads (release_producer)
+                            atomicOr(p.status, UAA_DEVFLAG_TIMEOUT);
+                            ok = false;
+                        }
+                        if (ok && p.fused && !counted && it == SH::kStages) {  // the ring is full: wait time
+                            count_in_and_advance(p, lens);
+                            counted = true;
+                        }
+                        if (ok && it >= SH::kStages &&
+                            !ptx::mbar_wait(bar_empty + 8 * s, ((it / SH::kStages) & 1) ^ 1, kWaitLimitCycles)) {
+                            atomicOr(p.status, UAA_DEVFLAG_TIMEOUT);
+                            ok = false;
+                        }
+                    }
+                    if (paged) ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    const uint32_t st = base + s * SH::kStageBytes;
+                    const uint32_t bar = bar_full + 8 * s;
+                    if (paged) {
+                        const int n = __popc(__ballot_sync(0xffffffffu, mine));
+                        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, n * sub * (SH::kTxBytes / TK));
+                        __syncwarp();
+                        const int ps_mask = (1 << p.pages.shift) - 1;
+                        if (mine)
+                            issue_rows<SH>(st, lane * sub, &tm_k, &tm_v, &tm_s, &tm_ks,
+                                           row < 0 ? -sub : static_cast<int>(row),
+                                           row < 0 ? 0 : static_cast<int>(row & ps_mask),
+                                           row < 0 ? -1 : static_cast<int>(row >> p.pages.shift), bar, stream_policy);
+                        continue;
+                    }
                     // 64-key tiles of this stage up to its run's last visible key: a run's
                     // last stage may need fewer than MG (its other rows are masked)
                     const int nt = MG > 1 ? min(MG, (sk.hi - key + kTileKeys - 1) / kTileKeys) : MG;
-                    if (!p.pages.table && nt < MG) {
+                    if (nt < MG) {
                         ptx::mbar_arrive_expect_tx(bar, nt * (SH::kTxBytes / MG));
                         for (int r0 = 0; r0 < nt * kTileKeys; r0 += kTileKeys)
                             issue_rows<SH>(st, r0, &tm_kt, &tm_vt, &tm_st, &tm_kst, row0 + key + r0, key + r0,
                                            head_row, bar, stream_policy);
-                    } else if (!p.pages.table) {
+                    } else {
                         ptx::mbar_arrive_expect_tx(bar, SH::kTxBytes);
                         issue_rows<SH>(st, 0, &tm_k, &tm_v, &tm_s, &tm_ks, row0 + key, key, head_row, bar,
                                        stream_policy);
-                    } else {
-                        ptx::mbar_arrive_expect_tx(bar, SH::kTxBytes);
-                        // paged: one load per page-aligned sub-tile; a sub-tile with no visible key
-                        // (beyond the unit's end or before its window) is not looked up and reads
-                        // as zeros from a negative row (masked by the consumers)
-                        const int sub = min(1 << p.pages.shift, kTileKeys);
-                        for (int r0 = 0; r0 < TK; r0 += sub) {
-                            const int ku = key + r0;
-                            long long row = -1;
-                            if (ku < sk.hi && ku + sub > sk.lo) {
-                                row = cache_row(p.pages, p.Hkv, p.cap, p.b_off + sg.b, sg.kvh, ku);
-                                if (row < 0) atomicOr(p.status, UAA_DEVFLAG_PAGE);
-                            }
-                            const int ps_mask = (1 << p.pages.shift) - 1;
-                            issue_rows<SH>(st, r0, &tm_k, &tm_v, &tm_s, &tm_ks, row < 0 ? -sub : static_cast<int>(row),
-                                           row < 0 ? 0 : static_cast<int>(row & ps_mask),
-                                           row < 0 ? -1 : static_cast<int>(row >> p.pages.shift), bar, stream_policy);
-                        }
                     }
                 }
                 pos += sg.n_st;
             }
+        }
+        if (lane == 0) {
             if (p.fused && !counted) count_in_and_advance(p, lens);
-            // Every copy this thread issued lands before the CTA may exit, also after a
+            // Every copy this warp issued lands before the CTA may exit, also after a
             // failed wait (then the consumers no longer wait for them): the last kStages
             // issued stages are the only ones not yet consumed, and once the producer
             // stops no barrier starts a new phase, so a phase that completed earlier
