@@ -526,7 +526,7 @@ cudaError_t launch_pages_reserve(const PageParams& p, int q_len, cudaStream_t s)
 cudaError_t launch_pages_compact(const PageParams& p, cudaStream_t s)
 {
     const cudaError_t e = launch_dependent(compact_kernel, dim3(1), dim3(kScanThreads), 0, s, p);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || p.B == 0) return e;
     return launch_dependent(rename_kernel, entries_grid(p), dim3(kPageThreads), 0, s, p);
 }
 

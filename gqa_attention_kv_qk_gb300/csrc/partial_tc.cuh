@@ -414,11 +414,11 @@ __device__ void prep_fused_q(const PartialParams& p, int b, int h0, int nh, bool
             }
         }
         __syncwarp();
+        // (a missing head's row is the zeros parked there)
 #pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < min(8, nh - hc0); ++i) {
             uint8_t* row = frag + (hc0 + i) * row_bytes;
             const float* raw = reinterpret_cast<const float*>(row);
-            const bool hv = hc0 + i < nh;
             float ya[NP], yb[NP];
 #pragma unroll
             for (int j = 0; j < NP; ++j) {
@@ -426,7 +426,7 @@ __device__ void prep_fused_q(const PartialParams& p, int b, int h0, int nh, bool
                 yb[j] = raw[ib[j]];
             }
             __syncwarp();  // every lane has its values before any writes fragments over them
-            if (p.qk_norm && hv) {
+            if (p.qk_norm) {
                 float ss = 0.f;
 #pragma unroll
                 for (int j = 0; j < NP; ++j) ss += ya[j] * ya[j] + yb[j] * yb[j];
@@ -440,8 +440,8 @@ __device__ void prep_fused_q(const PartialParams& p, int b, int h0, int nh, bool
             const size_t qoff = (static_cast<size_t>(b) * p.Hq + h0 + hc0 + i) * D;
 #pragma unroll
             for (int j = 0; j < NP; ++j) {
-                if (hv) rope_rotate(ya[j], yb[j], cs[lane + 32 * j]);
-                if (write_rot && hv) {
+                rope_rotate(ya[j], yb[j], cs[lane + 32 * j]);
+                if (write_rot) {
                     p.q_rot_out[qoff + ia[j]] = ya[j];
                     p.q_rot_out[qoff + ib[j]] = yb[j];
                 }

@@ -63,7 +63,7 @@ class DecodeLayer:
             t = cache.pop(name, None)
             if t is None:
                 return torch.zeros(shape, dtype=dtype, device=dev)
-            if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+            if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or t.device != dev:
                 raise ValueError(f"cache[{name!r}] is {tuple(t.shape)} {t.dtype} on {t.device}, the layer needs a "
                                  f"contiguous {tuple(shape)} {dtype} on its device")
             return t

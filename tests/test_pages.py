@@ -253,6 +253,21 @@ def test_pool_without_enough_pages():
 
 
 @pytest.mark.gpu
+def test_without_sequences():
+    """A table without rows: nothing to fork, trim or reserve, and pinned pages still move."""
+    from gqa_attention_kv_qk_gb300.pages import PageTable
+    pages = PageTable(torch.zeros((0, 3)), 16, 6, page_refs=torch.tensor([0, 1, 0, 0, 2, 0]))
+    pages.fork(torch.zeros(0, dtype=torch.int32, device="cuda"))
+    pages.trim(1, 0)
+    pages.reserve(5)
+    assert pages.counts.tolist()[0] == 0 and pages.counts.tolist()[2] == 0
+    pages.compact()
+    assert pages.device_status() == 0
+    assert pages.page_refs.tolist() == [2, 1, 0, 0, 0, 0]
+    assert pages.moves[:1].tolist() == [[4, 0]] and pages.counts.tolist()[:2] == [1, 2]
+
+
+@pytest.mark.gpu
 def test_bad_entries_are_flagged_and_left():
     pages = table_of([[0, 1], [2, -1]], [20, 5], 16, 8)
     pages.block_table[0, 1] = 99
