@@ -404,13 +404,21 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             const float mu = m == -INFINITY ? 0.f : m;
             {
-                float s4[4] = {0.f, 0.f, 0.f, 0.f};
+                // packed fp32 adds: the softmax's issue slots bound the kernel
+                float2 s01 = make_float2(0.f, 0.f), s23 = s01;
+                const float2 nmu = make_float2(-mu, -mu);
 #pragma unroll
-                for (int i = 0; i < KH; ++i) {
-                    x[i] = ptx::ex2(x[i] - mu);
-                    s4[i & 3] += x[i];
+                for (int i = 0; i < KH; i += 4) {
+                    const float2 a = ptx::add_f32x2(make_float2(x[i], x[i + 1]), nmu);
+                    const float2 b = ptx::add_f32x2(make_float2(x[i + 2], x[i + 3]), nmu);
+                    x[i] = ptx::ex2(a.x);
+                    x[i + 1] = ptx::ex2(a.y);
+                    x[i + 2] = ptx::ex2(b.x);
+                    x[i + 3] = ptx::ex2(b.y);
+                    s01 = ptx::add_f32x2(s01, make_float2(x[i], x[i + 1]));
+                    s23 = ptx::add_f32x2(s23, make_float2(x[i + 2], x[i + 3]));
                 }
-                l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                l += (s01.x + s01.y) + (s23.x + s23.y);
             }
             // value rows of keys at or past the sequence's end (unused slots, or another
             // head's rows) may hold anything, NaN included: zero them once they have

@@ -183,6 +183,20 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// Two fp32 sums in one instruction (each rounded as a plain fp32 add).
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // 1/x with the hardware approximation (rcp.approx.ftz: ~1 ulp).
 __device__ __forceinline__ float rcp(float x)
 {
