@@ -372,16 +372,13 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             float mh;
             {
+                static_assert(KH == 32, "32 = 8 runs of 3, then 8 more");
                 float t8[8];
 #pragma unroll
-                for (int a = 0; a < 8; ++a) {
-                    t8[a] = x[a];
+                for (int a = 0; a < 8; ++a) t8[a] = ptx::max3(x[a], x[a + 8], x[a + 16]);
 #pragma unroll
-                    for (int i = a + 8; i < KH; i += 8) t8[a] = fmaxf(t8[a], x[i]);
-                }
-#pragma unroll
-                for (int a = 0; a < 4; ++a) t8[a] = fmaxf(t8[a], t8[a + 4]);
-                mh = fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3]));
+                for (int a = 0; a < 4; ++a) t8[a] = ptx::max3(t8[a], x[24 + 2 * a], x[25 + 2 * a]);
+                mh = fmaxf(ptx::max3(ptx::max3(t8[0], t8[1], t8[2]), t8[3], t8[4]), ptx::max3(t8[5], t8[6], t8[7]));
             }
             // the row's maximum over its quarters, through two buffers in turn: a warp that
             // writes block j + 2's has passed block j + 1's barrier, so all have read block

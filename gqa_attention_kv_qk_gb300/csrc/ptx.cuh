@@ -183,6 +183,14 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// The largest of three (as fmaxf: a NaN operand is passed over).
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Two fp32 sums in one instruction (each rounded as a plain fp32 add).
 __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b)
 {
