@@ -195,6 +195,12 @@ uaa_status make_plan(const uaa_attn_desc* d, int batch, int q_len, int max_len, 
         p.heads_per_cta = 16;
         p.n_head_tiles = 2;
     }
+    // a 4-bit cache's codes are widened once per unit: three tiles where they make fewer
+    // units and their state fits two CTAs per SM (head_dim 64)
+    if (d->kv_dtype == UAA_DTYPE_Q4 && d->head_dim == 64 && (rows + 23) / 24 < (rows + 15) / 16) {
+        p.heads_per_cta = 24;
+        p.n_head_tiles = 3;
+    }
     p.head_groups = (rows + p.heads_per_cta - 1) / p.heads_per_cta;
     p.mg = p.kernel == 1 ? uaa::partial_tc_keys_per_stage(d->head_dim, d->kv_dtype, p.n_head_tiles) / uaa::kTileKeys : 1;
     p.per_sm = p.kernel == 0 ? 4 : uaa::partial_tc_ctas_per_sm(d->head_dim, d->kv_dtype, p.n_head_tiles);

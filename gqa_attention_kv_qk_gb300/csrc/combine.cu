@@ -30,7 +30,7 @@ constexpr int kCombineMinThreads = 128;
 constexpr int kCombineMaxThreads = 512;
 constexpr int kRecBatch = 4;     // records loaded together per output element
 
-// D, HC (query rows per unit: 8 or 16) are template arguments: divisions by them at
+// D, HC (query rows per unit: 8, 16 or 24) are template arguments: divisions by them at
 // run time were most of the code, and a kernel of a few microseconds that runs cold
 // pays for every line of it (5 us for a one-sequence step's combine, of 14).
 template <int D, int HC>
@@ -161,6 +161,7 @@ cudaError_t launch_combine(const CombineParams& p, cudaStream_t s)
         default: return cudaErrorInvalidValue;
         }
     }
+    if (p.heads_per_cta == 24) return p.D == 64 ? launch_combine_of<64, 24>(p, s) : cudaErrorInvalidValue;
     if (p.heads_per_cta != 16) return cudaErrorInvalidValue;
     switch (p.D) {
     case 64: return launch_combine_of<64, 16>(p, s);

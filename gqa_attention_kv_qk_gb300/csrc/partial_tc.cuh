@@ -90,7 +90,7 @@ constexpr int kKvBf16 = 0, kKvVq8 = 1, kKvQ8 = 2, kKvQ4 = 3;
 // where a warp's state is that large), whose warps take the registers of two.
 __host__ __device__ constexpr int ctas_per_sm(int D, int KV, int NHT)
 {
-    if (KV == kKvQ4) return D * NHT <= 128 ? 2 : 1;
+    if (KV == kKvQ4) return D * NHT <= 192 ? 2 : 1;
     return D == 256 || NHT == 2 ? 1 : 2;
 }
 
@@ -1800,6 +1800,8 @@ cudaError_t launch_one(const PartialParams& p, const PartialMaps& m, int n_ctas,
 template <int KV>
 size_t smem_bytes_kv(int D, int n_head_tiles)
 {
+    if constexpr (KV == kKvQ4)
+        if (n_head_tiles == 3) return D == 64 ? Shape<64, KV, 3>::kSmemBytes : 0;
     if (n_head_tiles == 2) {
         switch (D) {
         case 64: return Shape<64, KV, 2>::kSmemBytes;
@@ -1818,6 +1820,8 @@ size_t smem_bytes_kv(int D, int n_head_tiles)
 template <int KV, bool FIRST>
 cudaError_t launch_kv(const PartialParams& p, const PartialMaps& m, int n_head_tiles, int n_ctas, cudaStream_t s)
 {
+    if constexpr (KV == kKvQ4)
+        if (n_head_tiles == 3) return p.D == 64 ? launch_one<64, KV, 3, FIRST>(p, m, n_ctas, s) : cudaErrorInvalidValue;
     if (n_head_tiles == 2) {
         switch (p.D) {
         case 64: return launch_one<64, KV, 2, FIRST>(p, m, n_ctas, s);

@@ -144,6 +144,13 @@ CASES = {
     "chunk4-window": (dict(window=3), [254, 2], 4, 0),
     "chunk5-first": (dict(window=70, first_tokens=66), [500, 136, 135], 5, 0),
     "chunk33-d64": (dict(head_dim=64, n_q_heads=16), [200, 0], 33, 0),
+    # 24-row units (head_dim 64): one, a part of one, two, and a second one with a few rows
+    "chunk3-d64-g8": (dict(head_dim=64, n_q_heads=16, has_sink=True), [700, 255, 0, 62], 3, 0),
+    "chunk5-d64-g4-window": (dict(head_dim=64, window=9), [300, 4], 5, 0),
+    "chunk6-d64-g8-first": (dict(head_dim=64, n_q_heads=16, window=100, first_tokens=30), [500, 130, 129], 6, 0),
+    "chunk10-d64-g4-paged32": (dict(head_dim=64), [300, 60], 10, 32),
+    "d64-mha-chunk20": (dict(head_dim=64, n_q_heads=2), [300, 60], 20, 0),
+    "d64-g20": (dict(head_dim=64, n_q_heads=40, softcap=9.0), [300, 60], 1, 0),
     "chunk7-d256-norm": (dict(head_dim=256, qk_norm=True, norm_w_range=(0.5, 1.5)), [100, 3], 7, 0),
     "chunk3-interleaved-f32": (dict(rope_style="interleaved", io_dtype="f32", rotary_dim=64), [100, 3], 3, 0),
     "chunk3-rotary96": (dict(rotary_dim=96), [100, 3], 3, 0),     # halves of 48: the row-per-warp append
