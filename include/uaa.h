@@ -39,6 +39,9 @@
  *   - NeoX vs interleaved pairing and the llama3 parameters:
  *       FreeToken PR #722 "serve Llama and Mistral llama-arch GGUF", "Changes";
  *       llamay "Models and formats", "Architectures";
+ *   - the 4-bit cache (Q4), the first tokens kept behind a window and the page
+ *     operators (uaa_pages_*) are not on the pages: their rules stand at
+ *     uaa_q4_quantize, uaa_attn_desc.first_tokens and uaa_page_args;
  *   - per-head attention sink in the softmax denominator, YaRN for gpt-oss:
  *       llamay "Models and formats", "Architectures" (gpt-oss row);
  *   - the vq8 cache (int8 values, per-token per-head fp32 scale, keys exact)
@@ -56,7 +59,8 @@
  *     k_cache [B][Hkv][cap][D] (fp32, bf16 for BF16 and VQ8 caches, int8
  *     codes for Q8); v_cache [B][Hkv][cap][D] (fp32, bf16, or int8 codes for
  *     VQ8 and Q8); v_scale [B][Hkv][cap] fp32 (VQ8 and Q8); k_scale
- *     [B][Hkv][cap] fp32 (Q8 only); seq_lens [B] int32;
+ *     [B][Hkv][cap] fp32 (Q8 only); Q4: k_cache, v_cache [B][Hkv][cap][D / 2]
+ *     bytes, k_scale, v_scale [B][Hkv][cap][D / 32] fp16; seq_lens [B] int32;
  *     out [B][Hq][D] (out_dtype). Query head h reads kv head h / (Hq / Hkv).
  *   - Facts outside the supported ranges are refused with a status and a
  *     message naming the fact (uaa_last_error), never approximated.

@@ -421,3 +421,54 @@ def test_together(kv, captured):
         held = pages.held()
         assert held <= Bn * 5
         assert bool((pages.page_refs[:held] > 0).all()) and bool((pages.page_refs[held:] == 0).all())
+
+
+@pytest.mark.gpu
+def test_two_layers_on_one_table():
+    """Layers of different kinds share the table: the bookkeeping runs once, the copies
+    for each, and both keep their sequences' rows through forks and compaction."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    Bn, ps, P, N = 4, 32, 6, 30
+    base = dict(n_q_heads=4, n_kv_heads=2, head_dim=64, io_dtype="bf16", out_dtype="f32", rope_style="neox",
+                rope_theta=10000.0, seed=3, batch=Bn, seq_len=1)
+    pages = table_of([[-1] * P for _ in range(Bn)], [0] * Bn, ps, N)
+    layers = [DecodeLayer(dict(base, kv_dtype=kv), Bn, P * ps, page_size=ps, block_table=pages.block_table, n_pages=N,
+                          max_q_len=20) for kv in ("q4", "q8", "bf16", "f32", "vq8")]
+    rng = random.Random(5)
+    hist = [[([], []) for _ in range(Bn)] for _ in layers]
+    for step in range(12):
+        T = rng.choice([1, 2, 20])
+        parents = [rng.randrange(Bn) for _ in range(Bn)] if step % 3 == 2 else list(range(Bn))
+        pages.fork(torch.tensor(parents, dtype=torch.int32, device="cuda"))
+        pages.reserve(T)
+        start = pages.seq_lens.clone()
+        assert pages.device_status() == 0
+        for i, layer in enumerate(layers):
+            pages.copy_layer(layer)
+            layer.seq_lens.copy_(pages.seq_lens)
+            shape = lambda h: (Bn, T, h, 64) if T > 1 else (Bn, h, 64)
+            g = torch.Generator().manual_seed(1000 * step + i)
+            q, k, v = (torch.randn(shape(h), generator=g).to(torch.bfloat16).cuda() for h in (4, 2, 2))
+            layer.step(q, k, v, max_seq_len=P * ps - 20)
+            assert layer.device_status() == 0
+            rk, rv = (x.clone() for x in layer.read_rows(start, T))
+            hist[i] = [(list(hist[i][p][0]), list(hist[i][p][1])) for p in parents]
+            for b in range(Bn):
+                for t in range(T):
+                    hist[i][b][0].append(rk[b, t])
+                    hist[i][b][1].append(rv[b, t])
+        pages.seq_lens.copy_(layers[0].seq_lens)
+        if step % 2:
+            pages.compact()
+            for layer in layers:
+                pages.copy_layer(layer)
+        for i, layer in enumerate(layers):  # every row that a sequence has written, wherever it is now
+            n = max(len(h[0]) for h in hist[i])
+            rk, rv = layer.read_rows(None, n)
+            for b in range(Bn):
+                m = len(hist[i][b][0])
+                assert torch.equal(rk[b, :m], torch.stack(hist[i][b][0])), (step, i, b)
+                assert torch.equal(rv[b, :m], torch.stack(hist[i][b][1])), (step, i, b)
+        if int(pages.seq_lens.max()) > P * ps - 45:
+            break
+    assert step >= 5

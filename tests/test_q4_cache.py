@@ -404,3 +404,55 @@ def test_captured_and_replayed():
         assert torch.equal(graph.seq_lens, eager.seq_lens)
     for n in ("k_cache", "v_cache", "k_scale", "v_scale"):
         assert torch.equal(getattr(graph, n), getattr(eager, n))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [0, 64])
+def test_steps_of_different_lengths_in_turn(D, page):
+    """One layer and workspace through prefill chunks, draft tokens and single tokens
+    (other kernels, grids and workspace layouts in turn), from an empty cache."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    Bn, cap = 3, 512
+    cfg = config(batch=Bn, seq_len=0, head_dim=D, n_q_heads=16, first_tokens=9, window=200)
+    layer = DecodeLayer(cfg, Bn, cap, page_size=page, max_q_len=150)
+    g = torch.Generator().manual_seed(D + page)
+    n = 0
+    for T in (64, 1, 3, 2, 1, 150, 5, 1, 33, 8, 1, 1, 16):
+        shape = lambda h: (Bn, T, h, D) if T > 1 else (Bn, h, D)
+        q, k, v = (torch.randn(shape(h), generator=g).to(torch.bfloat16).cuda() for h in (16, 2, 2))
+        q_rot = torch.empty((Bn, T, 16, D), dtype=torch.float32, device="cuda")
+        out = layer.step(q, k, v, q_rot=q_rot)
+        torch.cuda.synchronize()
+        assert layer.device_status() == 0
+        kk, vv = plain64.cached_values(layer)
+        want = plain64.attend(q_rot, kk, vv, [n] * Bn, 200, 9)
+        err = (out.double().cpu().reshape(want.shape) - want).abs()
+        assert float(err.max()) <= TOL_MAX and float(err.mean()) <= TOL_MEAN, T
+        n += T
+        assert layer.seq_lens.tolist() == [n] * Bn
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 3])
+def test_static_scratch(T):
+    """uaa_decode_attn_static over a 4-bit cache under a window with first tokens."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    cfg = config(batch=3, seq_len=300, q_len=T, window=100, first_tokens=7, reproducible=True)
+    case = W.host_case(cfg, lens=[290, 0, 107])
+    a, b = DecodeLayer.for_case(case), DecodeLayer.for_case(case)
+    dev = {k: case[k].cuda() for k in ("q", "k_new", "v_new")}
+    want = a.step(dev["q"], dev["k_new"], dev["v_new"])
+    b._begin(dev["q"])
+    B.uaa_decode_attn_static(b.desc, b.args(dev["q"], dev["k_new"], dev["v_new"]), torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert torch.equal(b.out_for(T), want) and torch.equal(a.k_cache, b.k_cache) and torch.equal(a.v_scale, b.v_scale)
+    big = config(batch=3, seq_len=300, q_len=200)  # a prefill chunk's widened rows do not fit the built-in scratch
+    c = DecodeLayer.for_case(W.host_case(big, lens=[9, 0, 7]))
+    q = torch.zeros((3, 200, 8, 128), dtype=torch.bfloat16, device="cuda")
+    kv = torch.zeros((3, 200, 2, 128), dtype=torch.bfloat16, device="cuda")
+    c._begin(q)
+    args = c.args(q, kv, kv, max_seq_len=32000 - 200)
+    args.cache_capacity = 32000
+    st = B.uaa_decode_attn_static(c.desc, args, torch.cuda.current_stream(), check=False)
+    assert st == B.UAA_ERR_INVALID_ARGUMENT and "built-in scratch" in B.last_error()
