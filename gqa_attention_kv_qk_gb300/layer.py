@@ -76,10 +76,11 @@ class DecodeLayer:
             setattr(self, which + "_cache", tensor(which + "_cache", (*rows, width), dt))
             scale = {"q8": (rows, torch.float32), "q4": ((*rows, D // 32), torch.float16)}.get(kind)
             setattr(self, which + "_scale", tensor(which + "_scale", *scale) if scale else None)
+        given = cache.get("seq_lens") is not None
         self.seq_lens = tensor("seq_lens", (batch,), torch.int32)
         if any(t is not None for t in cache.values()):
             raise ValueError(f"a {kv} layer has no cache tensor named {sorted(cache)}")
-        self.max_len_hint = 0
+        self.max_len_hint = int(self.seq_lens.max()) if given and batch else 0
         self._args_cache = {}
         self._read_args = None
         self._reads = {}            # read_rows' tensors per row count
@@ -120,6 +121,7 @@ class DecodeLayer:
     def set_params(self, q_norm_w=None, k_norm_w=None, sink=None):
         to = lambda t: None if t is None else t.to(device=self.device, dtype=torch.float32).contiguous()
         self.q_norm_w, self.k_norm_w, self.sink = to(q_norm_w), to(k_norm_w), to(sink)
+        self._args_cache.clear()  # they hold the addresses of the ones before
 
     def _to_pool(self, logical, pool):
         """Logical rows [B][Hkv][cap][...] into a pool [n_pages][Hkv][page_size][...]."""
@@ -245,18 +247,19 @@ class DecodeLayer:
         sequence (start: int32 tensor [B] on the device, or None for 0), as
         [B][n][Hkv][D] tensors in the layer's out dtype; any cache kind, paged or not.
         Positions outside the cache, or on absent pages, read as zeros. The tensors are
-        the layer's own (one pair per n), overwritten by the next read of n rows, as a
-        step's output is by the next step."""
+        the layer's own (a pair for each of the first 16 values of n; new ones for
+        others), overwritten by the next read of n rows, as a step's output is by the
+        next step."""
         s = stream if stream is not None else B.current_stream(self._index)
         if start is not None and (start.dtype is not torch.int32 or start.shape != self.seq_lens.shape
-                                  or not start.is_cuda or not start.is_contiguous()):
+                                  or start.get_device() != self._index or not start.is_contiguous()):
             raise ValueError("start is not a contiguous int32 tensor [batch] on the device")
         got = self._reads.get(n)
         if got is None:
-            if len(self._reads) > 16:
-                self._reads.clear()
             shape = (self.batch, int(n), self.cfg["n_kv_heads"], self.cfg["head_dim"])
-            got = self._reads[n] = tuple(torch.empty(shape, dtype=self.out.dtype, device=self.device) for _ in "kv")
+            got = tuple(torch.empty(shape, dtype=self.out.dtype, device=self.device) for _ in "kv")
+            if len(self._reads) < 16:  # kept for good: a captured graph may write them
+                self._reads[n] = got
         if self._read_args is None:
             self._read_args = self._build_args(None, None, None, 0, None, None)
         B.uaa_cache_read(self.desc, self._read_args, B.ptr(start), int(n), B.ptr(got[0]), B.ptr(got[1]), s)

@@ -67,8 +67,8 @@ class PageTable:
 
     def fork(self, parents, stream=None):
         """Row b becomes a copy of row parents[b] (int32 [batch] on the device; -1: it ends)."""
-        if (parents.dtype is not torch.int32 or parents.shape != self.seq_lens.shape or not parents.is_cuda
-                or not parents.is_contiguous()):
+        if (parents.dtype is not torch.int32 or parents.shape != self.seq_lens.shape
+                or parents.get_device() != self.device.index or not parents.is_contiguous()):
             raise ValueError("parents is not a contiguous int32 tensor [batch] on the device")
         B.uaa_pages_fork(self.args, B.ptr(parents), self.ws, self._s(stream))
 
@@ -88,7 +88,7 @@ class PageTable:
         """The copies of the last reserve() or compact() in pools [n_pages][...] (up to eight)."""
         n, ptrs, sizes = self.n_pages, [], []
         for t in pools:
-            if t.size(0) != n or not t.is_contiguous() or not t.is_cuda:
+            if t.size(0) != n or not t.is_contiguous() or t.get_device() != self.device.index:
                 raise ValueError(f"a pool is {tuple(t.shape)} on {t.device}, not a contiguous [{n}][...] tensor on "
                                  "the device")
             ptrs.append(t.data_ptr())

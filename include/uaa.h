@@ -433,13 +433,15 @@ uaa_status uaa_pages_reserve(const uaa_page_args* args, int32_t q_len, const uaa
 
 /* Moves held pages to the front of the pool: with n of them (counts[1]), the i-th
  * held page at or past n goes to the i-th free page before n. Table and counts are
- * renamed; pages n .. n_pages - 1 are free afterwards. */
+ * renamed; pages n .. n_pages - 1 are free afterwards. A caller with pins of its own
+ * finds where they went in the moves. */
 uaa_status uaa_pages_compact(const uaa_page_args* args, const uaa_workspace* ws, cudaStream_t stream);
 
 /* Copies the pages of the last reserve or compact (counts[0] moves) in every given
  * pool: pool k holds page p in bytes p * page_bytes[k] .. (a multiple of 16). Up to
- * eight pools a call; call it for each layer. Moves set up by hand: no page may be
- * the destination of two, or of one and the source of another. */
+ * eight pools a call; call it for each layer, once and before the next operator on
+ * the table. Moves set up by hand: no page may be the destination of two, or of one
+ * and the source of another. */
 uaa_status uaa_pages_copy(const uaa_page_args* args, void* const* pools, const int64_t* page_bytes,
                           int32_t n_pools, const uaa_workspace* ws, cudaStream_t stream);
 

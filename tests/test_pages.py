@@ -193,7 +193,7 @@ def table_of(table, lens, ps, N):
 
 
 SHAPES = [(1, 1, 16, 1), (1, 3, 16, 7), (4, 5, 32, 33), (33, 7, 16, 400), (7, 300, 64, 5000), (300, 9, 128, 20000),
-          (1100, 4, 16, 40001)]
+          (1100, 4, 16, 40001), (130, 70, 16, 30000), (1200, 3, 16, 1500), (20, 80, 16, 1700)]
 
 
 @pytest.mark.gpu

@@ -348,6 +348,39 @@ def test_read_rows(kv, page, out):
 
 
 @pytest.mark.gpu
+def test_reads_keep_their_tensors():
+    """A captured read writes its pair at every replay, whatever was read since: the
+    layer never lets go of a pair. Row counts past the sixteenth get new tensors."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    layer = DecodeLayer.for_case(W.host_case(config(batch=2, seq_len=60), lens=[60, 3]))
+    first = layer.read_rows(None, 1)[0].data_ptr()
+    pairs = [layer.read_rows(None, n) for n in range(1, 40)]
+    assert layer.read_rows(None, 1)[0].data_ptr() == first and layer.read_rows(None, 16)[0] is pairs[15][0]
+    a, b = layer.read_rows(None, 30), layer.read_rows(None, 30)
+    assert a[0] is not b[0] and all(torch.equal(x, y) for x, y in zip(a, b))
+    start = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="on the device"):
+        layer.read_rows(start, 1)
+
+
+@pytest.mark.gpu
+def test_parameters_set_between_steps():
+    """A step takes the sink and the norm weights of the last set_params."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    cfg = config(batch=2, seq_len=60, has_sink=True, qk_norm=True)
+    case = W.host_case(cfg, lens=[60, 3])
+    dev = {k: case[k].cuda() for k in ("q", "k_new", "v_new")}
+    a, b = DecodeLayer.for_case(case), DecodeLayer.for_case(case)
+    a.step(dev["q"], dev["k_new"], dev["v_new"], advance_hint=False)
+    a.load_cache(case["k_values"], case["v_values"], case["lens"])
+    other = dict(q_norm_w=case["q_norm_w"] * 0.5, k_norm_w=case["k_norm_w"] * 1.5, sink=case["sink"] + 2.0)
+    for layer in (a, b):
+        layer.set_params(**other)
+    oa, ob = (x.step(dev["q"], dev["k_new"], dev["v_new"]) for x in (a, b))
+    assert torch.allclose(oa, ob, atol=1e-6)  # ranges may be cut elsewhere
+
+
+@pytest.mark.gpu
 def test_own_cache_tensors():
     """A layer works on the caller's tensors in place, and refuses ones that do not fit."""
     from gqa_attention_kv_qk_gb300.layer import DecodeLayer
@@ -357,7 +390,7 @@ def test_own_cache_tensors():
     own = {n: getattr(a, n).clone() for n in ("k_cache", "v_cache", "k_scale", "v_scale", "seq_lens")}
     b = DecodeLayer(cfg, 2, case["cap"], cache=own)
     dev = {k: case[k].cuda() for k in ("q", "k_new", "v_new")}
-    b.max_len_hint = 60
+    assert b.max_len_hint == 60  # of the caller's lengths
     oa, ob = a.step(dev["q"], dev["k_new"], dev["v_new"]), b.step(dev["q"], dev["k_new"], dev["v_new"])
     assert torch.allclose(oa, ob, atol=1e-6)  # ranges may be cut elsewhere
     for n, t in own.items():
