@@ -258,6 +258,13 @@ uaa_status make_plan(const uaa_attn_desc* d, int batch, int q_len, int max_len, 
 // The facts of a step's caches: their geometry, and the pointers that hold them.
 uaa_status check_cache_shape(const uaa_attn_desc* d, const uaa_step_args* a)
 {
+    // a ring stage that holds a sequence's last key reaches past it (two tiles; four over
+    // a 4-bit cache), and positions are 32-bit
+    const bool long_stage = d->kv_dtype == UAA_DTYPE_Q4 || d->first_tokens > 0;
+    const long long rows_max = 2147483647LL - (long_stage ? 8 : 2) * uaa::kTileKeys;
+    if (long_stage && a->cache_capacity > rows_max)
+        return fail(UAA_ERR_UNSUPPORTED, "cache_capacity=%d is above %lld, the largest of a 4-bit cache or with first_tokens",
+                    a->cache_capacity, rows_max);
     if (a->block_table) {
         const int ps = a->page_size;
         if (ps < 16 || ps > 4096 || (ps & (ps - 1)) != 0)
@@ -271,11 +278,11 @@ uaa_status check_cache_shape(const uaa_attn_desc* d, const uaa_step_args* a)
                         "cache_capacity=%d is not pages_per_seq=%d x page_size=%d", a->cache_capacity,
                         a->pages_per_seq, ps);
         if (a->n_pages <= 0) return fail(UAA_ERR_INVALID_ARGUMENT, "n_pages=%d is not positive", a->n_pages);
-        if ((long long)a->n_pages * d->n_kv_heads * ps > 2147483647LL - 2 * uaa::kTileKeys)
+        if ((long long)a->n_pages * d->n_kv_heads * ps > rows_max)
             return fail(UAA_ERR_UNSUPPORTED, "n_pages*n_kv_heads*page_size=%lld exceeds 2^31 cache rows",
                         (long long)a->n_pages * d->n_kv_heads * ps);
         if (!aligned16(a->block_table)) return fail(UAA_ERR_INVALID_ARGUMENT, "block_table is not 16-byte aligned");
-    } else if ((long long)a->batch * d->n_kv_heads * a->cache_capacity > 2147483647LL - 2 * uaa::kTileKeys) {
+    } else if ((long long)a->batch * d->n_kv_heads * a->cache_capacity > rows_max) {
         return fail(UAA_ERR_UNSUPPORTED, "batch*n_kv_heads*cache_capacity=%lld exceeds 2^31 cache rows",
                     (long long)a->batch * d->n_kv_heads * a->cache_capacity);
     }

@@ -344,7 +344,7 @@ __device__ __forceinline__ void store_frag_f16(uint8_t* row, int e, float x)
 // 8t .. 8t + 7 of a 32-dim group (t = lane % 4) and widens to the pairs (i, i + 4):
 // the row keeps each 8 dims in the order 0 4 1 5 2 6 3 7, so a lane's operands of
 // two k-steps are 16 contiguous bytes. One fp16 part: rounding q' moves a logit by
-// 2^-12 of its terms (~1e-4 for logits of a few units), far below what 4-bit keys do.
+// 2^-11 of its terms at most (~1e-3 for logits of a few units), below what 4-bit keys do.
 __device__ __forceinline__ void store_frag_q4(uint8_t* row, int e, float x)
 {
     const int i = e & 7;

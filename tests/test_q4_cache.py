@@ -46,6 +46,14 @@ def test_step_refusals():
     a = fake_args(k_scale=0x10000, block_table=0x10000, page_size=16, pages_per_seq=8, n_pages=16)
     assert B.uaa_decode_attn(d, a, WS, None, check=False) == B.UAA_ERR_UNSUPPORTED
     assert "page_size=16 is below 32" in B.last_error()
+    # a stage of 256 keys that holds the last one must not pass 2^31
+    d, cap = B.make_desc(config(n_kv_heads=1)), 2**31 - 256
+    for a, fact in ((fake_args(k_scale=0x10000, batch=1, cache_capacity=cap), f"cache_capacity={cap}"),
+                    (fake_args(k_scale=0x10000, block_table=0x10000, page_size=32, pages_per_seq=cap // 32, n_pages=8,
+                               cache_capacity=cap), f"cache_capacity={cap}"),
+                    (fake_args(k_scale=0x10000, batch=2, cache_capacity=cap // 2), "exceeds 2^31")):
+        assert B.uaa_decode_attn(d, a, WS, None, check=False) == B.UAA_ERR_UNSUPPORTED
+        assert fact in B.last_error()
 
 
 def test_quantize_refusals():
