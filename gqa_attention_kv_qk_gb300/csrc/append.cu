@@ -499,8 +499,9 @@ __host__ __device__ inline size_t staged_smem_bytes(int tps, int Hq, int Hkv, in
 
 // Stages of tokens_per_cta tokens (the last of a sequence may hold fewer); CTA c
 // takes stages c, c + gridDim.x, ... Inputs 16-byte aligned; NeoX rotation with
-// half_rot a multiple of 8.
-template <int D, typename T>
+// half_rot a multiple of 8. Q4: a 4-bit cache (a template argument: as a run-time
+// choice it cost the other caches' verify step 1 us of 11).
+template <int D, typename T, bool Q4>
 __global__ void __launch_bounds__(kStagedThreads, 2) append_staged_kernel(const AppendParams p)
 {
     constexpr int HALF = D / 2;
@@ -689,13 +690,13 @@ __global__ void __launch_bounds__(kStagedThreads, 2) append_staged_kernel(const 
             const bool stores = crow >= 0;
 
             // row maximum for the int8 codes (q8 keys after the rotation, vq8 / q8 values)
-            const bool quant = kind == 1 ? p.kv_dtype == UAA_DTYPE_Q8
-                                         : kind == 2 && (p.kv_dtype == UAA_DTYPE_VQ8 || p.kv_dtype == UAA_DTYPE_Q8);
+            const bool quant = Q4          ? false
+                               : kind == 1 ? p.kv_dtype == UAA_DTYPE_Q8
+                                           : kind == 2 && (p.kv_dtype == UAA_DTYPE_VQ8 || p.kv_dtype == UAA_DTYPE_Q8);
             // 4-bit groups of 32 dims: each run of 8 with those of the 4 neighbouring threads
             // (NeoX halves), or both runs with those of the next thread
-            const bool q4 = kind > 0 && p.kv_dtype == UAA_DTYPE_Q4;
             float g0 = 0.f, g1 = 0.f;
-            if (__any_sync(0xffffffffu, valid && q4)) {
+            if (Q4 && __any_sync(0xffffffffu, valid && kind > 0)) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     g0 = fmaxf(g0, fabsf(x0[j]));
@@ -711,7 +712,7 @@ __global__ void __launch_bounds__(kStagedThreads, 2) append_staged_kernel(const 
                 }
             }
             float amax = 0.f;
-            if (__any_sync(0xffffffffu, valid && quant)) {
+            if (!Q4 && __any_sync(0xffffffffu, valid && quant)) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fmaxf(fabsf(x0[j]), fabsf(x1[j])));
                 amax = group_max<U>(amax);
@@ -728,7 +729,7 @@ __global__ void __launch_bounds__(kStagedThreads, 2) append_staged_kernel(const 
                 }
             } else if (stores) {
                 const size_t slot = static_cast<size_t>(crow) * D;
-                if (q4) {
+                if (Q4) {
                     const __half s0 = q4_scale(g0), s1 = q4_scale(g1);
                     uint8_t* codes = static_cast<uint8_t*>(kind == 1 ? p.k_cache : p.v_cache) + slot / 2;
                     __half* sc = reinterpret_cast<__half*>(kind == 1 ? p.k_scale : p.v_scale) + slot / 32;
@@ -759,7 +760,7 @@ __global__ void __launch_bounds__(kStagedThreads, 2) append_staged_kernel(const 
             // recomputed from the staged row) reaches one; an unrotated, unnormalised
             // element is exact.
             unsigned near = 0;
-            if (stores && kind == 1 && p.kv_dtype != UAA_DTYPE_F32 && p.kv_dtype != UAA_DTYPE_Q8 && !q4) {
+            if (!Q4 && stores && kind == 1 && p.kv_dtype != UAA_DTYPE_F32 && p.kv_dtype != UAA_DTYPE_Q8) {
                 float a0[8], a1[8];
                 load8<T>(row, e0, a0);
                 load8<T>(row, e1, a1);
@@ -937,10 +938,11 @@ bool launch_staged(const AppendParams& p, cudaStream_t s, cudaError_t& err)
     const long long per_sm = std::max<long long>(1, std::min<long long>(2, smem_sm / static_cast<long long>(smem + 1024)));
     const long long ctas = std::min<long long>(n_stages, per_sm * n_sm);
     const dim3 grid(static_cast<unsigned>(ctas)), block(kStagedThreads);
-    const bool f32 = p.io_dtype == UAA_DTYPE_F32;
+    const bool f32 = p.io_dtype == UAA_DTYPE_F32, q4 = p.kv_dtype == UAA_DTYPE_Q4;
 #define UAA_STAGED_LAUNCH(DD)                                                                                          \
     do {                                                                                                               \
-        auto* kern = f32 ? append_staged_kernel<DD, float> : append_staged_kernel<DD, __nv_bfloat16>;                 \
+        auto* kern = q4 ? (f32 ? append_staged_kernel<DD, float, true> : append_staged_kernel<DD, __nv_bfloat16, true>) \
+                        : (f32 ? append_staged_kernel<DD, float, false> : append_staged_kernel<DD, __nv_bfloat16, false>); \
         err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));        \
         if (err == cudaSuccess) err = launch_dependent(kern, grid, block, smem, s, q);                                 \
     } while (0)
