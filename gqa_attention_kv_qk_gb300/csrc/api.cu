@@ -129,7 +129,7 @@ struct Plan {
     int prefill;         // a contiguous cache takes the query-tiled prefill kernel (no combine)
     int dense_rows;      // 4-bit caches there: rows per (sequence, kv head) widened in the workspace,
     int dense_batch;     // for so many sequences at a time (0 rows: other caches)
-    size_t off_status, off_qrot, off_prefix, off_rec_lse, off_rec_o, off_ranges, off_owners, off_balance, off_dense, total;
+    size_t off_status, off_counts, off_qrot, off_prefix, off_rec_lse, off_rec_o, off_ranges, off_owners, off_balance, off_dense, total;
     size_t prefix_stride, rec_lse_stride, rec_o_stride, ranges_stride, owners_stride;  // bytes per slice
 };
 
@@ -221,7 +221,12 @@ uaa_status make_plan(const uaa_attn_desc* d, int batch, int q_len, int max_len, 
     p.owners_stride = align256((size_t)p.slice * d->n_kv_heads * p.head_groups * 8);
     p.off_status = 0;
     p.off_balance = 256;
-    p.off_qrot = p.off_balance + balance_bytes(p.n_ctas);
+    // The splits' counters of the fp32 one-launch step (one per unit, at most P of its
+    // grid: f32_step_splits) are zero between launches, so no other geometry's arrays may
+    // reach them: they and what lies before them have places that depend on n_sm alone.
+    const int max_ctas = 4 * n_sm;
+    p.off_counts = p.off_balance + balance_bytes(max_ctas);
+    p.off_qrot = p.off_counts + align256((size_t)max_ctas * 4);
     p.off_prefix = p.off_qrot + align256(B * p.q_len * Hq * D * 4);
     p.off_rec_lse = p.off_prefix + p.n_slices * p.prefix_stride;
     p.off_rec_o = p.off_rec_lse + p.n_slices * p.rec_lse_stride;
@@ -929,7 +934,7 @@ uaa_status run_step_f32(const uaa_attn_desc* d, const uaa_step_args* a, const ua
     p.q_rot_out = a->q_rot;
     p.rec_o = reinterpret_cast<float*>(w + pl.off_rec_o);
     p.rec_lse = reinterpret_cast<float*>(w + pl.off_rec_lse);
-    p.unit_count = reinterpret_cast<unsigned*>(w + pl.off_owners);
+    p.unit_count = reinterpret_cast<unsigned*>(w + pl.off_counts);
     p.arrivals = reinterpret_cast<unsigned*>(w + pl.off_status) + 1;
     p.status = reinterpret_cast<unsigned*>(w + pl.off_status);
     rope_table(d, p.inv_freq_over_pi, &p.mscale);

@@ -212,7 +212,7 @@ struct StepF32Params {
     float* q_rot_out;       // optional [B][Hq][D]
     float* rec_o;           // [B][units][splits][8][D] (splits > 1)
     float* rec_lse;         // [B][units][splits][8]
-    unsigned* unit_count;   // [B][units][2]: word 0 counts a unit's finished splits (zero between launches)
+    unsigned* unit_count;   // [B][units]: a unit's finished splits (zero between launches)
     unsigned* arrivals;     // grid arrival counter (zero between launches)
     unsigned* status;
     double inv_freq_over_pi[kMaxHeadDim / 2];

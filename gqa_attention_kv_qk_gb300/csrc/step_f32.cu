@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kStepThreads) step_f32_kernel(const StepF32Par
     __threadfence();  // this thread's record rows, before the CTA counts in
     __syncthreads();
     if (tid == 0) {
-        unsigned* cnt = p.unit_count + 2 * static_cast<size_t>(ug);
+        unsigned* cnt = p.unit_count + ug;
         last = atomicAdd(cnt, 1u) == static_cast<unsigned>(S - 1);
         if (last) *cnt = 0u;  // ready for the next launch
     }

@@ -1,0 +1,96 @@
+"""One workspace through steps of different geometry: what a launch leaves in it for
+the next one survives the steps between, and its size covers every shorter step.
+
+Tolerance of the fp32 cache: the parity bar of the attention outputs (max 2e-3, mean
+2e-4 for values ~N(0, 1)); fp32 arithmetic over 700 keys is off by some 1e-6.
+"""
+import pytest
+import torch
+
+from gqa_attention_kv_qk_gb300 import binding as B
+from tests import plain64
+
+TOL_MAX, TOL_MEAN = 2e-3, 2e-4
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from gqa_attention_kv_qk_gb300 import build
+    build.build()
+
+
+def config(**kw):
+    cfg = dict(n_q_heads=32, n_kv_heads=8, head_dim=128, kv_dtype="f32", io_dtype="f32", out_dtype="f32",
+               rope_style="neox", rope_theta=10000.0, seed=41, batch=1, seq_len=64)
+    cfg.update(kw)
+    return cfg
+
+
+def filled_layer(cfg, batch, cap, n, max_q_len):
+    """A layer of `batch` sequences holding n random rows each."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    layer = DecodeLayer(cfg, batch, cap, max_q_len=max_q_len)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    for t in (layer.k_cache, layer.v_cache):
+        t[:, :, :n] = torch.randn(t[:, :, :n].shape, generator=g, device="cuda")
+    layer.set_lengths([n] * batch)
+    return layer
+
+
+def rows(cfg, batch, T, seed):
+    g = torch.Generator().manual_seed(seed)
+    shape = lambda h: (batch, T, h, cfg["head_dim"]) if T > 1 else (batch, h, cfg["head_dim"])
+    dt = torch.float32 if cfg["io_dtype"] == "f32" else torch.bfloat16
+    return [torch.randn(shape(h), generator=g).to(dt).cuda() for h in
+            (cfg["n_q_heads"], cfg["n_kv_heads"], cfg["n_kv_heads"])]
+
+
+def assert_step(layer, out, q_rot, n, what):
+    k, v = plain64.cached_values(layer)
+    want = plain64.attend(q_rot, k[:, :, :n + q_rot.shape[1]], v[:, :, :n + q_rot.shape[1]], [n] * layer.batch)
+    err = (out.double().cpu().reshape(want.shape) - want).abs()
+    assert float(err.max()) <= TOL_MAX and float(err.mean()) <= TOL_MEAN, (what, float(err.max()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,chunk", [(12, 3), (8, 64)])
+def test_fp32_steps_between_chunks(batch, chunk):
+    """The fp32 one-launch step merges a unit's splits when the last of them has counted
+    in. A chunk's split records (3 tokens, 12 sequences) or q rows (64 tokens) lie
+    where the shorter step has other arrays: the counts are still zero after it."""
+    cfg, n = config(), 700
+    layer = filled_layer(cfg, batch, 1024, n, chunk)
+    lay = B.uaa_get_workspace_layout(layer.desc, batch, n, 0, 1)
+    assert lay.step_splits > 1
+    layer.out.fill_(float("nan"))
+    for i, T in enumerate((chunk, 1, 1, chunk, 1)):
+        q, k, v = rows(cfg, batch, T, 10 * i + batch)
+        q_rot = torch.empty((batch, T, 32, 128), device="cuda")
+        out = layer.step(q, k, v, q_rot=q_rot)
+        torch.cuda.synchronize()
+        assert layer.device_status() == 0
+        assert_step(layer, out, q_rot, n, (i, T))
+        n += T
+
+
+@pytest.mark.gpu
+def test_fp32_step_after_another_desc_in_the_built_in_scratch():
+    """The same through uaa_decode_attn_static, whose one array serves every desc."""
+    cfg, n, batch = config(), 700, 8
+    layer = filled_layer(cfg, batch, 1024, n, 1)
+    other_cfg = config(kv_dtype="bf16", io_dtype="bf16")
+    other = filled_layer(other_cfg, batch, 256, 100, 40)
+    for i in range(2):
+        q, k, v = rows(other_cfg, batch, 40, i)  # its q rows take most of the array
+        other._begin(q)
+        B.uaa_decode_attn_static(other.desc, other.args(q, k, v), torch.cuda.current_stream())
+        other.max_len_hint += 40
+        layer.out.fill_(float("nan"))
+        q, k, v = rows(cfg, batch, 1, 5 + i)
+        q_rot = torch.empty((batch, 1, 32, 128), device="cuda")
+        layer._begin(q)
+        B.uaa_decode_attn_static(layer.desc, layer.args(q, k, v, q_rot=q_rot), torch.cuda.current_stream())
+        layer.max_len_hint += 1
+        torch.cuda.synchronize()
+        assert_step(layer, layer.out, q_rot, n, i)
+        n += 1
