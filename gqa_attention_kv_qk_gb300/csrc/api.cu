@@ -260,6 +260,20 @@ uaa_status make_plan(const uaa_attn_desc* d, int batch, int q_len, int max_len, 
     return UAA_OK;
 }
 
+// Bytes of a workspace that serves steps of q_len tokens and every shorter one: a
+// shorter step may need more (24-row units over a 4-bit cache, where a longer one
+// takes 16-row units). 0 on refused facts.
+size_t workspace_bytes(const uaa_attn_desc* d, int batch, int q_len, int max_len, int n_sm)
+{
+    size_t bytes = 0;
+    for (int t = q_len; t >= (q_len > 1 ? 1 : q_len); --t) {  // the longest first: its refusal is the caller's
+        Plan pl{};
+        if (make_plan(d, batch, t, max_len, n_sm, &pl) != UAA_OK) return 0;
+        if (pl.total > bytes) bytes = pl.total;
+    }
+    return bytes;
+}
+
 // The facts of a step's caches: their geometry, and the pointers that hold them.
 uaa_status check_cache_shape(const uaa_attn_desc* d, const uaa_step_args* a)
 {
@@ -1088,10 +1102,8 @@ uaa_status uaa_decode_attn(const uaa_attn_desc* desc, const uaa_step_args* args,
 size_t uaa_workspace_size(const uaa_attn_desc* desc, int32_t batch, int32_t max_seq_len, int32_t n_sm,
                           int32_t q_len)
 {
-    Plan pl{};
     if (n_sm <= 0) n_sm = device_sm_count();
-    if (make_plan(desc, batch, q_len, max_seq_len, n_sm, &pl) != UAA_OK) return 0;
-    return pl.total;
+    return workspace_bytes(desc, batch, q_len, max_seq_len, n_sm);
 }
 
 int32_t uaa_num_splits(const uaa_attn_desc* desc, int32_t batch, int32_t max_seq_len, int32_t n_sm, int32_t q_len)
@@ -1140,7 +1152,7 @@ uaa_status uaa_get_workspace_layout(const uaa_attn_desc* desc, int32_t batch, in
     layout->owners_offset = pl.off_owners;
     layout->owners_stride = pl.owners_stride;
     layout->balance_offset = pl.off_balance;
-    layout->total_bytes = pl.total;
+    layout->total_bytes = workspace_bytes(desc, batch, q_len, max_seq_len, n_sm);
     return UAA_OK;
 }
 

@@ -277,7 +277,7 @@ typedef struct {
     size_t owners_stride;
     size_t balance_offset;    /* range-balance state of the tensor-core kernel (opaque), right
                                  after the status word so that it survives a change of batch */
-    size_t total_bytes;
+    size_t total_bytes;       /* uaa_workspace_size: this step's, or that of a shorter one that needs more */
 } uaa_workspace_layout;
 
 /* Step 1 (append). Writes the k/v rows at slot seq_lens[b], increments seq_lens,

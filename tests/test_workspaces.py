@@ -94,3 +94,41 @@ def test_fp32_step_after_another_desc_in_the_built_in_scratch():
         torch.cuda.synchronize()
         assert_step(layer, layer.out, q_rot, n, i)
         n += 1
+
+
+@pytest.mark.parametrize("kv", ["f32", "bf16", "vq8", "q8", "q4"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_size_never_falls_with_longer_steps(kv, D):
+    """A workspace sized for q_len serves every step of at most q_len tokens."""
+    for G, Hkv, batch, n_sm, max_len in ((1, 1, 1, 152, 100), (1, 8, 3, 152, 100), (2, 4, 16, 148, 4095),
+                                         (4, 8, 16, 152, 4095), (8, 8, 4, 148, 4095), (8, 1, 1030, 152, 8000),
+                                         (16, 2, 2, 152, 300), (20, 1, 1, 152, 5)):
+        d = B.make_desc(config(kv_dtype=kv, head_dim=D, n_q_heads=G * Hkv, n_kv_heads=Hkv))
+        sizes = [B.uaa_workspace_size(d, batch, max_len, n_sm, t) for t in (*range(1, 140), 300, 1000)]
+        assert sizes[0] > 0 and sizes == sorted(sizes), (G, Hkv, batch)
+        for t in (1, 5, 40):
+            assert B.uaa_get_workspace_layout(d, batch, max_len, n_sm, t).total_bytes == sizes[t - 1]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv_heads,longest", [(64, 8, 4), (16, 4, 8), (2, 1, 16), (1, 1, 32)])
+def test_shorter_steps_than_the_longest(heads, kv_heads, longest):
+    """Over a 4-bit cache at head_dim 64, 17-24 rows take 24-row units and 25-32 rows
+    16-row ones, in a smaller workspace: a layer made for the longer steps serves both.
+    (One sequence: its q rows do not make up for the units. Bar: q' and P are one fp16
+    part each, 4e-3 and 4e-4 for values ~N(0, 1).)"""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    cfg = config(kv_dtype="q4", io_dtype="bf16", head_dim=64, n_q_heads=heads, n_kv_heads=kv_heads)
+    layer = DecodeLayer(cfg, 1, 512, max_q_len=longest)
+    n, G = 0, heads // kv_heads
+    for i, T in enumerate((longest, 24 // G, 1, longest, 17 // G + 1, 24 // G)):
+        q, k, v = rows(cfg, 1, T, i)
+        q_rot = torch.empty((1, T, heads, 64), device="cuda")
+        out = layer.step(q, k, v, q_rot=q_rot)
+        torch.cuda.synchronize()
+        assert layer.device_status() == 0
+        kk, vv = plain64.cached_values(layer)
+        want = plain64.attend(q_rot, kk, vv, [n])
+        err = (out.double().cpu().reshape(want.shape) - want).abs()
+        assert float(err.max()) <= 4e-3 and float(err.mean()) <= 4e-4, T
+        n += T
