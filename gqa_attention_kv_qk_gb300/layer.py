@@ -123,26 +123,38 @@ class DecodeLayer:
         self.q_norm_w, self.k_norm_w, self.sink = to(q_norm_w), to(k_norm_w), to(sink)
         self._args_cache.clear()  # they hold the addresses of the ones before
 
+    def _entries(self):
+        """The block table's entries as one index per logical page, and which of them
+        name a page (a trimmed, ended or fresh row holds -1)."""
+        e = self.block_table.reshape(-1).long()
+        return e, (e >= 0) & (e < self.n_pages)
+
     def _to_pool(self, logical, pool):
-        """Logical rows [B][Hkv][cap][...] into a pool [n_pages][Hkv][page_size][...]."""
+        """Logical rows [B][Hkv][cap][...] into a pool [n_pages][Hkv][page_size][...]; rows
+        of absent pages go nowhere."""
         Bn, Hkv, ps, P = self.batch, logical.shape[1], self.page_size, self.pages_per_seq
         rest = tuple(logical.shape[3:])
         x = logical.reshape(Bn, Hkv, P, ps, *rest).transpose(1, 2).reshape(Bn * P, Hkv, ps, *rest)
-        pool.index_copy_(0, self.block_table.reshape(-1).long(), x.to(device=pool.device, dtype=pool.dtype))
+        e, held = self._entries()
+        pool.index_copy_(0, e[held], x.to(device=pool.device, dtype=pool.dtype)[held])
 
     def logical(self, name: str):
         """A cache tensor ("k_cache", "v_cache", "k_scale", "v_scale") as logical
-        rows [B][Hkv][cap][...] (a gathered copy for a paged layer)."""
+        rows [B][Hkv][cap][...] (a gathered copy for a paged layer, zeros where the
+        table has no page)."""
         t = getattr(self, name)
         if t is None or not self.page_size:
             return t
         Bn, P, ps = self.batch, self.pages_per_seq, self.page_size
-        x = t.index_select(0, self.block_table.reshape(-1).long())
+        e, held = self._entries()
+        x = t.index_select(0, e.masked_fill(~held, 0))
+        x.masked_fill_(~held.reshape(-1, *[1] * (x.dim() - 1)), 0)
         Hkv, rest = x.shape[1], tuple(x.shape[3:])
         return x.reshape(Bn, P, Hkv, ps, *rest).transpose(1, 2).reshape(Bn, Hkv, P * ps, *rest)
 
     def load_cache(self, k, v, lens):
-        """Copy host caches (logical rows [B][Hkv][cap][D]) in. For a vq8 layer `v`
+        """Copy host caches (logical rows [B][Hkv][cap][D]) in; rows on pages that a paged
+        layer's table does not hold are left out. For a vq8 layer `v`
         holds fp32 values, and for a q8 or q4 layer `k` too, quantised on the device by
         uaa_vq8_quantize or uaa_q4_quantize (the append's own rules)."""
         D = self.cfg["head_dim"]
