@@ -6,6 +6,8 @@ makes: build the layer, load or grow its cache, then `step(q, k_new, v_new)`.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import binding as B
@@ -19,6 +21,19 @@ def _require_cuda(device):
         raise RuntimeError("DecodeLayer needs a CUDA device; libuaa has no CPU implementation")
     d = torch.device(device)
     return d if d.index is not None or d.type != "cuda" else torch.device("cuda", torch.cuda.current_device())
+
+
+def _memory_of(stream, index):
+    """The context in which new tensors take memory that is in order with `stream` (a
+    stream object or a raw handle of device `index`; None: the current one). Memory of
+    the current stream may have work pending there that another stream does not wait
+    for, and goes back to it while the other's is."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(handle, index) if handle else torch.cuda.default_stream(index)
+    return torch.cuda.stream(stream)
 
 
 class DecodeLayer:
@@ -188,20 +203,23 @@ class DecodeLayer:
         self.max_len_hint = int(lens.max()) if lens.numel() else 0
 
     # ------------------------------------------------------------ calls
-    def out_for(self, q_len: int):
-        """The layer's output rows for steps of q_len tokens per sequence."""
+    def out_for(self, q_len: int, stream=None):
+        """The layer's output rows for steps of q_len tokens per sequence (made for the
+        given stream if there are none yet)."""
         o = self._outs.get(q_len)
         if o is None:
-            o = self._outs[q_len] = torch.empty((self.batch, q_len, *self.out.shape[1:]), dtype=self.out.dtype,
-                                                device=self.device)
+            with _memory_of(stream, self._index):
+                o = self._outs[q_len] = torch.empty((self.batch, q_len, *self.out.shape[1:]), dtype=self.out.dtype,
+                                                    device=self.device)
         return o
 
-    def _begin(self, q):
-        """Tokens per sequence of a step's q ([B][Hq][D] or [B][T][Hq][D])."""
+    def _begin(self, q, stream=None):
+        """Tokens per sequence of a step's q ([B][Hq][D] or [B][T][Hq][D]); the step runs on `stream`."""
         T = int(q.shape[1]) if q.dim() == 4 else 1
         if T > self.max_q_len:
             raise ValueError(f"{T} tokens per sequence, the layer was built for max_q_len={self.max_q_len}")
         self.q_len = T
+        self.out_for(T, stream)
         return T
 
     def args(self, q, k_new, v_new, max_seq_len=None, q_rot=None, out=None) -> B.UaaStepArgs:
@@ -244,7 +262,7 @@ class DecodeLayer:
         per sequence ([B][Hq][D]) or T tokens ([B][T][Hq][D], causal within the
         chunk); the output rows ([B][Hq][D] or [B][T][Hq][D]) go to `out` if given."""
         s = stream if stream is not None else B.current_stream(self._index)
-        T = self._begin(q)
+        T = self._begin(q, stream)
         want = self.out_for(T)
         if out is not None:
             assert out.shape == want.shape and out.dtype == want.dtype and out.is_contiguous()
@@ -261,7 +279,8 @@ class DecodeLayer:
         Positions outside the cache, or on absent pages, read as zeros. The tensors are
         the layer's own (a pair for each of the first 16 values of n; new ones for
         others), overwritten by the next read of n rows, as a step's output is by the
-        next step."""
+        next step; work on another stream than the read's waits for it, and keeps them
+        (record_stream) for as long as it uses them."""
         s = stream if stream is not None else B.current_stream(self._index)
         if start is not None and (start.dtype is not torch.int32 or start.shape != self.seq_lens.shape
                                   or start.get_device() != self._index or not start.is_contiguous()):
@@ -269,7 +288,8 @@ class DecodeLayer:
         got = self._reads.get(n)
         if got is None:
             shape = (self.batch, int(n), self.cfg["n_kv_heads"], self.cfg["head_dim"])
-            got = tuple(torch.empty(shape, dtype=self.out.dtype, device=self.device) for _ in "kv")
+            with _memory_of(stream, self._index):
+                got = tuple(torch.empty(shape, dtype=self.out.dtype, device=self.device) for _ in "kv")
             if len(self._reads) < 16:  # kept for good: a captured graph may write them
                 self._reads[n] = got
         if self._read_args is None:
@@ -279,14 +299,14 @@ class DecodeLayer:
 
     def append(self, q, k_new, v_new, stream=None, q_rot=None):
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        self._begin(q)
+        self._begin(q, stream)
         B.uaa_rope_qk_norm_append(self.desc, self.args(q, k_new, v_new, q_rot=q_rot), self.ws, s)
 
     def append_partial(self, q, k_new, v_new, stream=None, q_rot=None):
         """Steps 1 and 2 (one fused kernel for bf16 / vq8 / q8 caches and one token);
         follow with combine()."""
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        self._begin(q)
+        self._begin(q, stream)
         B.uaa_decode_attn_append_partial(self.desc, self.args(q, k_new, v_new, q_rot=q_rot), self.ws, s)
 
     def partial(self, stream=None):

@@ -76,3 +76,84 @@ def test_absent_pages(kv):
     for a, b in zip(plain64.cached_values(layer), plain64.cached_values(full)):
         assert torch.equal(a.transpose(1, 2)[held], b.transpose(1, 2)[held])
     assert layer.device_status() == 0
+
+
+# ---------------------------------------------------------------- other streams
+
+def test_new_tensors_belong_to_the_stream_that_writes_them(monkeypatch):
+    """The tensors that a read or a step makes on first use are allocated in the context
+    of the stream it was given: memory of the current stream may have work pending that
+    the other does not wait for, and returns to it under the other's pending writes."""
+    import contextlib
+
+    from gqa_attention_kv_qk_gb300 import layer as L
+    active, made = [], []
+
+    @contextlib.contextmanager
+    def entered(stream):
+        active.append(stream)
+        yield
+        active.pop()
+
+    empty = torch.empty
+
+    def recorded(*shape, **kw):
+        made.append(active[-1] if active else None)
+        return empty(*shape, **kw)
+
+    class Stream:
+        cuda_stream = 0x1234
+
+    monkeypatch.setattr(torch.cuda, "stream", entered)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, index: (handle, index))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda index: ("default", index))
+    monkeypatch.setattr(torch, "empty", recorded)
+    monkeypatch.setattr(B, "uaa_cache_read", lambda *a, **k: 0)
+    monkeypatch.setattr(B, "uaa_decode_attn", lambda *a, **k: 0)
+    monkeypatch.setattr(B, "current_stream", lambda index: 7)
+    layer = L.DecodeLayer.__new__(L.DecodeLayer)
+    layer.cfg, layer.batch, layer.max_q_len, layer._index, layer.device = config(), 1, 4, 0, torch.device("cpu")
+    layer.out, layer._reads, layer._read_args, layer.seq_lens = empty(1, 4, 64), {}, object(), torch.zeros(1)
+    layer.desc = layer.ws = None
+    layer._outs, layer.max_len_hint, layer._args = {1: layer.out}, 0, lambda *a: None
+    for n, stream, want in ((1, Stream(), (0x1234, 0)), (2, None, None), (3, 0x77, (0x77, 0)), (4, 0, ("default", 0))):
+        layer.read_rows(None, n, stream=stream)
+        assert made == [want, want], n
+        made.clear()
+        if n > 1:
+            layer.step(torch.zeros(1, n, 4, 64), None, None, stream=stream, max_seq_len=5)
+            assert made == [want], n
+            made.clear()
+    layer.read_rows(None, 3, stream=Stream())  # kept: no new ones
+    assert not made
+
+
+@pytest.mark.gpu
+def test_reads_on_another_stream():
+    """A read that is pending on a side stream owns its tensors: their memory is not
+    handed out on the current stream meanwhile, and was not taken from under work
+    pending there."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    layer = DecodeLayer.for_case(W.host_case(config(batch=2, seq_len=200), lens=[200, 150]))
+    want = {n: [x.clone() for x in layer.read_rows(None, n)] for n in range(1, 60)}  # the first 16 counts are kept
+    torch.cuda.synchronize()
+    side, wait = torch.cuda.Stream(), 100_000_000  # about 50 ms
+    for n in (40, 41, 42):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(wait)
+        got = layer.read_rows(None, n, stream=side)
+        shape, dtype = got[0].shape, got[0].dtype
+        del got
+        mine = [torch.full(shape, 7.0, dtype=dtype, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(bool((x == 7.0).all()) for x in mine)
+        del mine
+    for n in (50, 51, 52):
+        old = [torch.empty(want[n][0].shape, device="cuda") for _ in range(4)]
+        torch.cuda._sleep(wait)
+        for x in old:
+            x.fill_(9.0)
+        del old, x
+        got = layer.read_rows(None, n, stream=side.cuda_stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want[n]))
