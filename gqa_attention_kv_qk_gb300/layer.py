@@ -222,6 +222,17 @@ class DecodeLayer:
         self.out_for(T, stream)
         return T
 
+    def _bound(self, T, stream=None):
+        """The bound on the lengths before a step of T tokens. max_len_hint grows with every
+        step and knows nothing of rows that ended or went back to a shorter parent:
+        where the capacity would end by it, the lengths themselves are read (which waits
+        for the stream; not in a capture)."""
+        if self.max_len_hint + T > self.capacity and self.batch:
+            with _memory_of(stream, self._index):
+                if not torch.cuda.is_current_stream_capturing():
+                    self.max_len_hint = max(0, int(self.seq_lens.max()))
+        return self.max_len_hint
+
     def args(self, q, k_new, v_new, max_seq_len=None, q_rot=None, out=None) -> B.UaaStepArgs:
         """The step's argument struct (a copy of one built once per distinct set of pointers)."""
         msl = self.max_len_hint if max_seq_len is None else int(max_seq_len)
@@ -260,13 +271,16 @@ class DecodeLayer:
     def step(self, q, k_new, v_new, stream=None, max_seq_len=None, advance_hint=True, q_rot=None, out=None):
         """One step (append, split-K partials, combine) on `stream` for q of one token
         per sequence ([B][Hq][D]) or T tokens ([B][T][Hq][D], causal within the
-        chunk); the output rows ([B][Hq][D] or [B][T][Hq][D]) go to `out` if given."""
+        chunk); the output rows ([B][Hq][D] or [B][T][Hq][D]) go to `out` if given.
+        max_seq_len: a bound on the lengths before the step, for a capture or where the
+        caller knows one (default: the layer's own, read from the device when the
+        capacity would end by it)."""
         s = stream if stream is not None else B.current_stream(self._index)
         T = self._begin(q, stream)
         want = self.out_for(T)
         if out is not None:
             assert out.shape == want.shape and out.dtype == want.dtype and out.is_contiguous()
-        msl = self.max_len_hint if max_seq_len is None else int(max_seq_len)
+        msl = self._bound(T, stream) if max_seq_len is None else int(max_seq_len)
         B.uaa_decode_attn(self.desc, self._args(q, k_new, v_new, msl, q_rot, want if out is None else out), self.ws, s)
         if advance_hint and max_seq_len is None:
             self.max_len_hint += T
@@ -299,14 +313,14 @@ class DecodeLayer:
 
     def append(self, q, k_new, v_new, stream=None, q_rot=None):
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        self._begin(q, stream)
+        self._bound(self._begin(q, stream), stream)
         B.uaa_rope_qk_norm_append(self.desc, self.args(q, k_new, v_new, q_rot=q_rot), self.ws, s)
 
     def append_partial(self, q, k_new, v_new, stream=None, q_rot=None):
         """Steps 1 and 2 (one fused kernel for bf16 / vq8 / q8 caches and one token);
         follow with combine()."""
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        self._begin(q, stream)
+        self._bound(self._begin(q, stream), stream)
         B.uaa_decode_attn_append_partial(self.desc, self.args(q, k_new, v_new, q_rot=q_rot), self.ws, s)
 
     def partial(self, stream=None):

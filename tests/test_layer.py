@@ -157,3 +157,93 @@ def test_reads_on_another_stream():
         got = layer.read_rows(None, n, stream=side.cuda_stream)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want[n]))
+
+
+# ---------------------------------------------------------------- length bounds
+
+def test_length_bound_on_the_host(monkeypatch):
+    """The bound that a step passes on: it grows by the step's tokens, and where the
+    capacity would end by it, it is the lengths' own largest again."""
+    from gqa_attention_kv_qk_gb300 import layer as L
+    passed, capturing = [], [False]
+    monkeypatch.setattr(B, "uaa_decode_attn", lambda *a, **k: 0)
+    monkeypatch.setattr(B, "uaa_rope_qk_norm_append", lambda *a, **k: 0)
+    monkeypatch.setattr(B, "current_stream", lambda index: 7)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: 7)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    layer = L.DecodeLayer.__new__(L.DecodeLayer)
+    layer.batch, layer.capacity, layer.max_q_len, layer._index, layer.device = 2, 64, 7, 0, torch.device("cpu")
+    layer.out = torch.empty(2, 4, 64)
+    layer._outs, layer.max_len_hint, layer.desc, layer.ws, layer.q_len = {1: layer.out}, 0, None, None, 1
+    layer._args = lambda q, k, v, msl, q_rot, out: passed.append(msl)
+    layer.args = lambda q, k, v, q_rot=None: passed.append(layer.max_len_hint)
+    q = torch.zeros(2, 7, 4, 64)
+    for i in range(40):  # rows that start over every third step
+        layer.seq_lens = torch.tensor([i % 3 * 7, 0], dtype=torch.int32)
+        layer.step(q, None, None)
+        assert layer.seq_lens[0] <= passed[-1] <= 64 - 7
+    assert passed[:9] == [7 * i for i in range(9)] and passed[9] == 0
+    layer.max_len_hint = 60
+    layer.append(q, None, None)
+    assert passed[-1] == layer.seq_lens[0]
+    layer.seq_lens, layer.max_len_hint = torch.tensor([60, 5], dtype=torch.int32), 63
+    layer.step(q, None, None)
+    assert passed[-1] == 60                     # full: refused by the call
+    layer.seq_lens, layer.max_len_hint = torch.tensor([-1, -1], dtype=torch.int32), 63
+    layer.step(q, None, None)
+    assert passed[-1] == 0
+    layer.max_len_hint, capturing[0] = 63, True
+    layer.step(q, None, None)
+    assert passed[-1] == 63                     # a capture does not wait
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("entry", ["step", "split", "side"])
+def test_loop_of_forks_outlives_the_capacity(entry):
+    """Rows that end and start over take more steps than one sequence has room for: the
+    step's bound on the lengths follows them. A row that is full is still refused.
+    (Bar of fp32 outputs of values ~N(0, 1): 2e-3.)"""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    from gqa_attention_kv_qk_gb300.pages import PageTable
+    from tests import plain64
+    Bn, ps, P, T = 3, 16, 4, 7
+    pages = PageTable(torch.full((Bn, P), -1), ps, 16)
+    layer = DecodeLayer(config(batch=Bn), Bn, P * ps, page_size=ps, block_table=pages.block_table, n_pages=16,
+                        max_q_len=T, cache=dict(seq_lens=pages.seq_lens))
+    side = torch.cuda.Stream() if entry == "side" else None
+    lens = [0] * Bn
+    for i in range(40):
+        parents = [-1 if lens[b] + T > P * ps or (i + b) % 5 == 4 else b for b in range(Bn)]
+        lens = [n if p >= 0 else 0 for n, p in zip(lens, parents)]
+        par = torch.tensor(parents, dtype=torch.int32, device="cuda")
+        q, k, v = (torch.randn((Bn, T, h, 64), generator=torch.Generator().manual_seed(10 * i + h)).to(torch.bfloat16).cuda()
+                   for h in (4, 2, 2))
+        q_rot = torch.empty((Bn, T, 4, 64), device="cuda")
+        torch.cuda.synchronize()
+        pages.fork(par, stream=side)
+        pages.reserve(T, stream=side)
+        pages.copy_layer(layer, stream=side)
+        if entry == "split":
+            layer.append(q, k, v, q_rot=q_rot)
+            layer.partial()
+            out = layer.combine()
+        else:
+            out = layer.step(q, k, v, q_rot=q_rot, stream=side)
+        torch.cuda.synchronize()
+        assert layer.device_status() == 0 and pages.device_status() == 0
+        kk, vv = plain64.cached_values(layer)
+        want = plain64.attend(q_rot, kk, vv, lens)
+        assert float((out.double().cpu() - want).abs().max()) <= 2e-3, i
+        lens = [n + T for n in lens]
+        assert pages.seq_lens.tolist() == lens
+    layer.set_lengths([P * ps - T + 1, 0, 0])
+    with pytest.raises(B.UaaError, match="does not fit cache_capacity=64"):
+        layer.step(q, k, v)
+    with pytest.raises(B.UaaError, match="does not fit cache_capacity=64"):
+        layer.append(q, k, v)
+    g = torch.cuda.CUDAGraph()  # in a capture the layer's bound stands as it is
+    layer.set_lengths([0] * Bn)
+    layer.max_len_hint = P * ps
+    with pytest.raises(B.UaaError, match="does not fit"):
+        with torch.cuda.graph(g):
+            layer.step(q, k, v)
