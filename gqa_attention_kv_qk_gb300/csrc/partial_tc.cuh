@@ -871,14 +871,19 @@ __device__ __forceinline__ void q4_group_sums(uint8_t* frag, int row_bytes, int 
 // 64 + u as the operand keeps sums to a few hundred times q', 2^-24 of which is far
 // below q's own fp16 rounding.
 //
-// Softmax. The reference maximum m is raised only where a logit exceeds it by more
-// than 2^8 (weights then stay below 2^8, sums in fp32): most groups need no exchange
-// between lanes. The weights go to the tensor core as one fp16 part (2^-11).
+// Softmax. The reference m lies 2^-7 below the largest logit when it was last raised,
+// and is raised only where a logit exceeds that by more than 2^8: most groups need no
+// exchange between lanes. The weights go to the tensor core as one fp16 part; below
+// 2^15 they fit, and those down to 2^-21 of the largest keep 11 bits (smaller ones
+// 2^-32 of it absolute), so that a long tail behind one dominant key is not rounded
+// away while the sums, in fp32, keep it.
 //
 // Values. ldmatrix.trans hands a lane the 4 dims 32 c + 4 g .. + 3 (a b16 element)
 // of keys 2t and 2t + 1; nibble i of both is the fp16 pair of dim 4 g + i, widened to
 // code x scale exactly. m-tile 2 c has dims 4 g (row g) and 4 g + 1 (row g + 8) of
 // group c, m-tile 2 c + 1 dims 4 g + 2 and 4 g + 3.
+constexpr float kQ4Below = 7.f;
+
 template <class SH, int NTW, bool FIRST, bool GENERAL>
 __device__ __forceinline__ void consume_q4(const PartialParams& p, uint32_t kaddr, uint32_t vaddr, const uint8_t* ksc,
                                            const uint8_t* vsc, int kbase, int lo, int hi, bool causal,
@@ -943,16 +948,17 @@ __device__ __forceinline__ void consume_q4(const PartialParams& p, uint32_t kadd
 #pragma unroll
     for (int nt = 0; nt < NTW; ++nt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) raise |= fmaxf(x[nt][j], x[nt][j + 2]) > m[nt][j] + 8.f;
+        for (int j = 0; j < 2; ++j) raise |= fmaxf(x[nt][j], x[nt][j + 2]) > m[nt][j] + (8.f + kQ4Below);
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int nt = 0; nt < NTW; ++nt) {
             float f[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float mx = fmaxf(m[nt][j], fmaxf(x[nt][j], x[nt][j + 2]));
+                float mx = fmaxf(x[nt][j], x[nt][j + 2]);
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                mx = fmaxf(m[nt][j], mx - kQ4Below);
                 f[j] = mx == -INFINITY ? 1.f : ptx::ex2(m[nt][j] - mx);
                 m[nt][j] = mx;
                 l[nt][j] *= f[j];

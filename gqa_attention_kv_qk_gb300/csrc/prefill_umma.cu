@@ -101,6 +101,8 @@ __device__ __forceinline__ void um_split_trunc(float x0, float x1, uint32_t& hi,
     lo = __byte_perm(__float_as_uint(x0 - __uint_as_float(h0)), __float_as_uint(x1 - __uint_as_float(h1)), 0x7632);
 }
 
+constexpr float kF16Below = 7.f;
+
 __device__ __forceinline__ uint32_t um_pack_f16(float lo, float hi)
 {
     __half2 v = __floats2half2_rn(lo, hi);
@@ -391,13 +393,19 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             for (int o = 1; o < kUmSplit; ++o) mx = fmaxf(mx, xb[((h + o) % kUmSplit) * kUmRows + r]);
             if (!kTwoBuffers) ptx::named_barrier_sync(quad_bar, 32 * kUmSplit);
 
-            // raise the reference maximum where a logit exceeds it by more than 2^8
-            const bool raise = mx > m + 8.f;
-            const float f = raise ? ptx::ex2(m - mx) : 1.f;  // 0 while m = -inf
+            // raise the reference m where a logit exceeds the largest at its last raise by
+            // more than 2^8. An fp16 P is taken relative to 2^-7 of that logit: its weights
+            // reach up to 2^15 and those down to 2^-21 of the largest keep 11 bits (below,
+            // 2^-32 of it absolute), so that a long tail behind one dominant key is not
+            // rounded away while l keeps it.
+            constexpr float kBelow = F16 ? kF16Below : 0.f;
+            const bool raise = mx > m + (8.f + kBelow);
+            const float m_new = F16 ? mx - kBelow : mx;
+            const float f = raise ? ptx::ex2(m - m_new) : 1.f;  // 0 while m = -inf
             const bool rescale = j > 0 && __any_sync(0xffffffffu, raise && m != -INFINITY);
             if (raise) {
                 l *= f;
-                m = mx;
+                m = m_new;
             }
             const float mu = m == -INFINITY ? 0.f : m;
             {

@@ -497,3 +497,47 @@ def test_static_scratch(T):
     args.cache_capacity = 32000
     st = B.uaa_decode_attn_static(c.desc, args, torch.cuda.current_stream(), check=False)
     assert st == B.UAA_ERR_INVALID_ARGUMENT and "built-in scratch" in B.last_error()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["prefill", "decode"])
+def test_long_tail_behind_a_dominant_key(kind):
+    """One key holds almost all of a row's mass and the rest lies in a long tail of equal
+    weights of w = 2^-24.8 of it: fp16 weights relative to the dominant one would round
+    each to 2^-24, 1.7 times as much.
+
+    Values are 7 in the tail and 0 at the dominant key, so the output is 7 r / (1 + r)
+    with r = n w. Tolerance: a tail weight's own rounding (2^-11 of it) and that of q'
+    (2^-11 of a logit of 24.8 in log2, times ln 2: 17.2 times as much) move r by
+    r 2^-11 18.2; fp32 sums of equal terms over 2^13 accumulations by r 2^-11 at most."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    if kind == "prefill":
+        Bn, Hkv, n, T = 1, 1, 2 ** 17, 128     # the query-tiled kernel
+    else:                                      # as many units as ranges: each range is a whole unit
+        Hkv, n, T = 8, 2 ** 15, 1
+        Bn = 2 * torch.cuda.get_device_properties(0).multi_processor_count // Hkv
+    cfg = config(n_q_heads=Hkv, n_kv_heads=Hkv, head_dim=64, rotary_dim=2, batch=Bn, reproducible=True)
+    layer = DecodeLayer(cfg, Bn, n + 128, max_q_len=T)
+    assert B.uaa_get_workspace_layout(layer.desc, Bn, n, 0, T).kernel == (2 if T > 1 else 1)
+    layer.k_cache.fill_(0x88)                  # code 0
+    layer.k_cache[:, :, 0, 1] = 0x8F           # the first key: 7 in dim 2, which no position turns
+    layer.v_cache.fill_(0xFF)                  # code 7
+    layer.v_cache[:, :, 0] = 0x88
+    layer.k_scale.fill_(1.0)
+    layer.v_scale.fill_(1.0)
+    layer.set_lengths([n] * Bn)
+    shape = (Bn, T, Hkv, 64) if T > 1 else (Bn, Hkv, 64)
+    q, k, v = (torch.zeros(shape, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    q[..., 2] = 19.625                         # 19.625 * 7 / sqrt(64) log2(e) = 24.77
+    v.fill_(7.0)
+    out = layer.step(q, k, v)
+    torch.cuda.synchronize()
+    assert layer.device_status() == 0
+    keys, values = (torch.zeros(1, 1, n + T, 64, dtype=torch.float64) for _ in range(2))
+    keys[:, :, 0, 2], values[:, :, 1:] = 7.0, 7.0
+    for t in sorted({0, T // 2, T - 1}):
+        want = float(plain64.attend(q[:1].reshape(1, T, Hkv, 64)[:, t:t + 1, :1], keys, values, [n + t])[0, 0, 0, 0])
+        r = want / (7.0 - want)
+        assert 0.9 * (n + t) * 2.0 ** -24.8 < r < 1.1 * (n + t) * 2.0 ** -24.7
+        got = out.double().cpu().reshape(Bn, T, Hkv, 64)[:, t]
+        assert float((got - want).abs().max()) <= 7 * r * 2.0 ** -11 * 19.2, (t, want, float(got.min()), float(got.max()))
