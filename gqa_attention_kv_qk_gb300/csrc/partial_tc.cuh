@@ -46,8 +46,10 @@
 //       is then a pair of adjacent codes), one byte permute and one fp16
 //       subtract per pair widen the codes exactly, and the PV product runs in
 //       fp16. The per-key scale is folded into P; to keep P * scale inside
-//       [0, 1] it is divided by the warp's running maximum scale r, and O is
-//       kept in units of r (a new maximum rescales O as a new logit maximum does).
+//       [0, 2^14] it is divided by the warp's running maximum scale r and taken
+//       2^14 times, and O is kept in units of r 2^-14 (a new maximum rescales O as
+//       a new logit maximum does). (In [0, 1] fp16's smallest step, 2^-24, rounded
+//       away a long tail of keys behind a dominant one.)
 //     The warp that owns the new key's row copies the staged rows over that
 //     row of the unit's last stage after it lands (the tile load brought
 //     whatever the slot held before the step).
@@ -209,8 +211,11 @@ __device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uin
     lo = pack_bf16(x0 - h0, x1 - h1);
 }
 
+// The largest product of a weight and a relative value scale (int8 values).
+constexpr float kPScale = 16384.f;
+
 // The same split into fp16 hi + lo parts (|x| below the fp16 range: the P
-// weights in [0, 1], or q' rows for int8 keys).
+// weights in [0, kPScale], or q' rows for int8 keys).
 __device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint32_t& lo)
 {
     __half2 h = __floats2half2_rn(x0, x1);
@@ -1424,7 +1429,7 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
             for (int mi = 0; mi < KS; ++mi) o[nt][mi][0] = o[nt][mi][1] = o[nt][mi][2] = o[nt][mi][3] = 0.f;
         }
-        float r_scale = 0.f;  // vq8: the warp's running maximum value scale (O is kept in units of it)
+        float r_scale = 0.f;  // vq8: the warp's running maximum value scale (O is kept in units of it / kPScale)
 
         for (int k = 0; k < sg.n_st; ++k, ++it) {
             const int s = it % SH::kStages;
@@ -1558,8 +1563,8 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     r_ratio = r_new > 0.f ? r_scale * inv : 1.f;
 #pragma unroll
                     for (int mg = 0; mg < MG; ++mg) {
-                        w_g[mg] *= inv;
-                        w_g8[mg] *= inv;
+                        w_g[mg] *= inv * kPScale;
+                        w_g8[mg] *= inv * kPScale;
                     }
                     r_scale = r_new;
                 }
@@ -1736,7 +1741,8 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         const int hc = (nt0 + nt) * 8 + 2 * t + (e & 1);
                         const int d = Q4 ? 32 * (mi >> 1) + 4 * g + 2 * (mi & 1) + (e >> 1)
                                     : VQ8 ? 16 * mi + 2 * g + (e >> 1) : 16 * mi + g + 8 * (e >> 1);
-                        if (d >= c0 && d < c0 + RC) red_o[(kgrp * HC + hc) * (RC + 4) + d - c0] = o[nt][mi][e] * o_unit;
+                        if (d >= c0 && d < c0 + RC) red_o[(kgrp * HC + hc) * (RC + 4) + d - c0] =
+                            VQ8 ? o[nt][mi][e] * (1.f / kPScale) * o_unit : o[nt][mi][e];
                     }
             ptx::named_barrier_sync(1, CW * 32);
             for (int idx = threadIdx.x; idx < nh * RC; idx += CW * 32) {

@@ -131,3 +131,48 @@ def test_first_tokens(name, entry):
     half_step = want.abs() * torch.finfo(torch.bfloat16).eps / 2 if cfg["out_dtype"] == "bf16" else 0.0
     assert ((err - half_step) <= TOL_MAX).all(), float(err.max())
     assert float((err - half_step).clamp(min=0).mean()) <= TOL_MEAN
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["vq8", "q8"])
+def test_long_tail_behind_a_first_token(kv):
+    """The first token holds almost all of a row's mass, the window a long tail of equal
+    weights of w = 2^-24.8 of it: as fp16 numbers relative to the first token's, hi + lo
+    parts both end at 2^-24, and every tail weight was 1.7 times as large.
+
+    Values are 127 s in the tail and 0 at the first token, so the output is
+    127 s r / (1 + r) with r = n w. Tolerance: rounding q' to 16 bits moves a logit of
+    24.8 (log2) by 24.8 2^-16, fp32 rounding of the products below that: r by r 2^-11 at
+    most; the weights' hi + lo parts and fp32 sums of 2^13 equal terms: r 2^-11."""
+    from gqa_attention_kv_qk_gb300 import build
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    build.build()
+    Hkv, n = 8, 2 ** 15
+    Bn = 2 * torch.cuda.get_device_properties(0).multi_processor_count // Hkv  # a range per unit
+    cfg = config(kv_dtype=kv, n_q_heads=Hkv, n_kv_heads=Hkv, head_dim=64, rotary_dim=2, batch=Bn, reproducible=True,
+                 window=n - 100, first_tokens=1)
+    layer = DecodeLayer(cfg, Bn, n + 128)
+    s = 1.0 / 127
+    if kv == "q8":
+        layer.k_scale.fill_(7.0 / 127)
+        layer.k_cache[:, :, 0, 2] = 127        # dim 2, which no position turns
+        key = float(torch.tensor(7.0 / 127)) * 127
+    else:
+        layer.k_cache[:, :, 0, 2] = 7.0
+        key = 7.0
+    layer.v_cache.fill_(127)
+    layer.v_cache[:, :, 0] = 0
+    layer.v_scale.fill_(s)
+    layer.set_lengths([n] * Bn)
+    q, k, v = (torch.zeros((Bn, Hkv, 64), dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    q[..., 2] = 19.625                         # 19.625 * 7 / sqrt(64) log2(e) = 24.77
+    v.fill_(1.0)
+    out = layer.step(q, k, v)
+    torch.cuda.synchronize()
+    assert layer.device_status() == 0
+    keys, values = (torch.zeros(1, 1, n + 1, 64, dtype=torch.float64) for _ in range(2))
+    keys[:, :, 0, 2], values[:, :, 1:] = key, float(torch.tensor(s)) * 127
+    want = float(plain64.attend(q[:1, None, :1], keys, values, [n], n - 100, 1)[0, 0, 0, 0])
+    r = want / (1.0 - want)
+    assert 0.9 * n * 2.0 ** -24.8 < r < 1.1 * n * 2.0 ** -24.7
+    assert float((out.double().cpu() - want).abs().max()) <= r * 2.0 ** -10, (want, float(out.min()), float(out.max()))
