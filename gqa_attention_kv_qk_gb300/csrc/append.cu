@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 2) append_kernel(const Appe
     // the step's tokens take positions L .. L + q_len - 1; a sequence whose tokens do
     // not all fit the cache is not appended (and not advanced)
     const int L = p.seq_lens[b];
-    const bool fits = L >= 0 && L + p.q_len <= p.cap;
+    const bool fits = L >= 0 && L <= p.cap - p.q_len;
     if (threadIdx.x == 0 && grp == 0 && part == 0) {
         if (!fits) atomicOr(p.status, UAA_DEVFLAG_CAPACITY);
         else if (L > p.max_len) atomicOr(p.status, UAA_DEVFLAG_LEN_HINT);
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 2) append_kernel(const Appe
     __threadfence();
     for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
         const int n = p.seq_lens[i];
-        if (n >= 0 && n + p.q_len <= p.cap) p.seq_lens[i] = n + p.q_len;
+        if (n >= 0 && n <= p.cap - p.q_len) p.seq_lens[i] = n + p.q_len;
     }
 }
 
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kStagedThreads, 2) append_staged_kernel(const 
         // the stage's tokens take positions L + t0 .. ; a sequence whose tokens do not
         // all fit the cache is not appended (its q rows rotate at position 0)
         const int L = ctl[2 + (i & 1)];
-        const bool fits = L >= 0 && L + p.q_len <= p.cap;
+        const bool fits = L >= 0 && L <= p.cap - p.q_len;
         if (tid == 0 && t0 == 0) {
             if (!fits)
                 atomicOr(p.status, UAA_DEVFLAG_CAPACITY);
@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(kStagedThreads, 2) append_staged_kernel(const 
     __threadfence();
     for (int i = tid; i < p.B; i += blockDim.x) {
         const int n = p.seq_lens[i];
-        if (n >= 0 && n + p.q_len <= p.cap) p.seq_lens[i] = n + p.q_len;
+        if (n >= 0 && n <= p.cap - p.q_len) p.seq_lens[i] = n + p.q_len;
     }
 }
 

@@ -153,13 +153,12 @@ __global__ void __launch_bounds__(kRowThreads) widen_q4_kernel(const WidenParams
     const int bh = blockIdx.y, b = bh / p.Hkv, h = bh - b * p.Hkv;
     const bool is_v = blockIdx.z == 1;
     const int n = p.seq_lens[b];
-    const int L = n - p.q_len;
     if (n > p.row_cap) {  // longer than the caller's bound: the prefill kernel leaves zero rows
         if (blockIdx.x == 0 && h == 0 && !is_v && threadIdx.x == 0 && n <= p.cap)
             atomicOr(p.status, UAA_DEVFLAG_LEN_HINT);
         return;
     }
-    if (L < 0 || row0 >= n) return;
+    if (n < p.q_len || row0 >= n) return;
     const Keys keys = key_range(n, p.window, p.first_tokens);  // the chunk's union
     const int block = row0 / kPrefillKeys * kPrefillKeys;
     if (block + kPrefillKeys <= keys.lo && block >= keys.first) return;

@@ -463,11 +463,12 @@ __host__ __device__ inline int cta_of(long long x, long long T, int P)
 }
 
 // Visible keys of a sequence of n keys, clamped to the cache (a longer length is
-// flagged by the caller).
+// flagged by the caller); none where the window lies past it, or n < 0.
 __device__ __forceinline__ Keys visible_keys(int n, int window, int first_tokens, int cap)
 {
     Keys k = key_range(n, window, first_tokens);
     if (k.hi > cap) k.hi = cap;
+    if (k.hi <= k.lo) k.lo = k.hi = k.first = 0;  // callers add to lo
     return k;
 }
 

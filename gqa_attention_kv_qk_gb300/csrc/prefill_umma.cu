@@ -185,7 +185,7 @@ prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     // past them); a sequence the append could not take keeps its length and gets zero rows.
     const int L_after = p.seq_lens[b];
     const int L = L_after - p.q_len;
-    const bool valid = L >= 0 && L_after <= p.cap && (!F16 || L_after <= p.row_cap);
+    const bool valid = L_after >= p.q_len && L_after <= p.cap && (!F16 || L_after <= p.row_cap);
     const int r_first = rb * kUmRows, r_last = min(rows, r_first + kUmRows) - 1;
     // keys the block sees: [0, first) and [lo, hi) (Keys), in n_f and n_st - n_f key
     // blocks; block j starts at key block_key(j) and its keys lie in the run of its part

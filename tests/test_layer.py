@@ -247,3 +247,67 @@ def test_loop_of_forks_outlives_the_capacity(entry):
     with pytest.raises(B.UaaError, match="does not fit"):
         with torch.cuda.graph(g):
             layer.step(q, k, v)
+
+
+# ---------------------------------------------------------------- lengths outside the cache
+
+def step_cases():
+    for kv in ("f32", "bf16", "vq8", "q8", "q4"):
+        for T in (1, 4, 70):  # one token, a short chunk, 140 rows per kv head
+            for page in (0, 32):
+                for win, first in ((0, 0), (50, 9)):
+                    yield kv, T, page, win, first
+
+
+def step_pair(kv, T, page, win, first, odd):
+    """Two layers alike; in the second one, sequence 1 has the length `odd` (the first one's is 20)."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    lens = [130, 20, 57]
+    cfg = config(kv_dtype=kv, io_dtype="f32" if kv == "f32" else "bf16", batch=3, seq_len=130, q_len=T, page_size=page,
+                 window=win, first_tokens=first, reproducible=True)
+    case = W.host_case(cfg, lens=lens)
+    a, b = DecodeLayer.for_case(case), DecodeLayer.for_case(case)
+    b.seq_lens[1] = odd
+    b.out_for(T).fill_(7.0)
+    return a, b, [case[k].cuda() for k in ("q", "k_new", "v_new")]
+
+
+def compare_pair(a, b, T, odd, run):
+    before = [t.clone() for t in (b.k_cache, b.v_cache)]
+    want, got = run(a), run(b)
+    torch.cuda.synchronize()
+    assert a.device_status() == 0
+    assert b.seq_lens.tolist() == [130 + T, odd, 57 + T]
+    for x, y in ((a.logical("k_cache"), b.logical("k_cache")), (a.logical("v_cache"), b.logical("v_cache"))):
+        assert torch.equal(x[::2], y[::2])
+    for t, old in zip((b.logical("k_cache"), b.logical("v_cache")), before):
+        if not b.page_size:
+            assert torch.equal(t[1], old[1])
+    # ranges are cut elsewhere: each side's weights are within 2^-11 (one fp16 part) or
+    # 2^-16 (two parts) of the exact ones, and values within +-4.5
+    eps = 2.0 ** -11 if a.desc.kv_dtype == B.DTYPE["q4"] else 2.0 ** -16
+    assert float((got[::2] - want[::2]).abs().max()) <= 9 * eps
+    return got
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("entry", ["step", "split"])
+@pytest.mark.parametrize("odd", [2**31 - 1, 2**31 - 30, -2**31])
+def test_lengths_at_the_ends_of_int32(entry, odd):
+    """No sum of a length and a step's tokens wraps: such a sequence is not appended and
+    the others are as they are alone; with a window it sees nothing."""
+    for kv, T, page, win, first in step_cases():
+        a, b, x = step_pair(kv, T, page, win, first, odd)
+
+        def run(layer):
+            if entry == "step":
+                return layer.step(*x, max_seq_len=130, advance_hint=False)
+            layer.append(*x)
+            layer.partial()
+            return layer.combine()
+
+        got = compare_pair(a, b, T, odd, run)
+        flags = b.device_status()
+        assert odd < 0 or flags & B.UAA_DEVFLAG_CAPACITY, (kv, T, page, win)
+        if odd < 0 or win:
+            assert not got[1].any(), (kv, T, page, win)
