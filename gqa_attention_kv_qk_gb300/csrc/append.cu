@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 2) append_kernel(const Appe
     const int L = p.seq_lens[b];
     const bool fits = L >= 0 && L <= p.cap - p.q_len;
     if (threadIdx.x == 0 && grp == 0 && part == 0) {
-        if (!fits) atomicOr(p.status, UAA_DEVFLAG_CAPACITY);
+        if (!fits && L >= 0) atomicOr(p.status, UAA_DEVFLAG_CAPACITY);  // L < 0: idle
         else if (L > p.max_len) atomicOr(p.status, UAA_DEVFLAG_LEN_HINT);
     }
 
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kStagedThreads, 2) append_staged_kernel(const 
         const int L = ctl[2 + (i & 1)];
         const bool fits = L >= 0 && L <= p.cap - p.q_len;
         if (tid == 0 && t0 == 0) {
-            if (!fits)
+            if (!fits && L >= 0)  // L < 0: idle
                 atomicOr(p.status, UAA_DEVFLAG_CAPACITY);
             else if (L > p.max_len)
                 atomicOr(p.status, UAA_DEVFLAG_LEN_HINT);

@@ -503,7 +503,7 @@ __device__ inline void build_stage_prefix(const int* seq_lens, int B, int window
             if (b < B) {
                 const int n = seq_lens[b];
                 lens[b] = n;
-                if (status && (fused ? (n < 0 || n >= cap) : n > cap)) atomicOr(status, UAA_DEVFLAG_CAPACITY);
+                if (status && (fused ? n >= cap : n > cap)) atomicOr(status, UAA_DEVFLAG_CAPACITY);
                 if (status && fused && n >= 0 && n < cap && n > max_len) atomicOr(status, UAA_DEVFLAG_LEN_HINT);
                 v = units * stages_of(sequence_keys(n, window, first_tokens, cap, fused), mg);
                 if (owners && v == 0)

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kStepThreads) step_f32_kernel(const StepF32Par
     // length that fitted.
     auto count_in = [&]() {
         if (u == 0 && s == 0) {
-            if (!fits) atomicOr(p.status, UAA_DEVFLAG_CAPACITY);
+            if (!fits && L >= 0) atomicOr(p.status, UAA_DEVFLAG_CAPACITY);  // L < 0: idle
             else if (L > p.max_len) atomicOr(p.status, UAA_DEVFLAG_LEN_HINT);
         }
         __threadfence();

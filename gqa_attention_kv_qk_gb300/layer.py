@@ -95,7 +95,7 @@ class DecodeLayer:
         self.seq_lens = tensor("seq_lens", (batch,), torch.int32)
         if any(t is not None for t in cache.values()):
             raise ValueError(f"a {kv} layer has no cache tensor named {sorted(cache)}")
-        self.max_len_hint = int(self.seq_lens.max()) if given and batch else 0
+        self.max_len_hint = max(0, int(self.seq_lens.max())) if given and batch else 0
         self._args_cache = {}
         self._read_args = None
         self._reads = {}            # read_rows' tensors per row count
@@ -195,12 +195,12 @@ class DecodeLayer:
         put(v, self.v_cache, self.v_scale)
         lens = torch.as_tensor(lens, dtype=torch.int32)
         self.seq_lens.copy_(lens)
-        self.max_len_hint = int(lens.max()) if lens.numel() else 0
+        self.max_len_hint = max(0, int(lens.max())) if lens.numel() else 0
 
     def set_lengths(self, lens):
         lens = torch.as_tensor(lens, dtype=torch.int32)
         self.seq_lens.copy_(lens)
-        self.max_len_hint = int(lens.max()) if lens.numel() else 0
+        self.max_len_hint = max(0, int(lens.max())) if lens.numel() else 0
 
     # ------------------------------------------------------------ calls
     def out_for(self, q_len: int, stream=None):

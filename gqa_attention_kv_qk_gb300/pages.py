@@ -15,6 +15,11 @@ page_size=..., block_table=pages.block_table, n_pages=...)`), then between steps
 A layer's `seq_lens` is its own (a step advances it); one layer may be built on
 the table's (`cache=dict(seq_lens=pages.seq_lens)`), the others follow with
 `layer.seq_lens.copy_(pages.seq_lens)` after a fork.
+
+A row that ended has length 0 and starts over with the next tokens: reserve gives it
+a page like any other. One that is to stay idle takes a negative length
+(`pages.seq_lens.masked_fill_(parents < 0, -1)`): it asks for no page, a step neither
+appends to it nor reads it, and its output rows are zero.
 """
 from __future__ import annotations
 

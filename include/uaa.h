@@ -199,7 +199,9 @@ typedef struct {
     void* v_cache;            /* [B][Hkv][cap][D] */
     float* v_scale;           /* [B][Hkv][cap], VQ8 and Q8 (Q4: fp16 [B][Hkv][cap][D / 32]) */
     int32_t cache_capacity;   /* cap: slots per (sequence, kv head), a multiple of 4 */
-    int32_t* seq_lens;        /* [B]: tokens cached before the step; the append adds 1 */
+    int32_t* seq_lens;        /* [B]: tokens cached before the step; the append adds 1. A negative
+                                 length is an idle row: not appended, not read, its output rows zero,
+                                 no flag */
     int32_t max_seq_len;      /* host bound on seq_lens[b] before the step (+1 must fit cap) */
     void* out;                /* [B][Hq][D] out_dtype */
     float* q_rot;             /* optional [B][Hq][D] fp32: the normed, rotated q rows */
@@ -411,7 +413,8 @@ typedef struct {
 size_t uaa_pages_workspace_size(int32_t batch, int32_t pages_per_seq, int32_t n_pages);
 
 /* Every row b of the table, and its length, becomes a copy of row parents[b] as it
- * was before the call; parents[b] = b keeps a row, -1 ends it (no pages, length 0).
+ * was before the call; parents[b] = b keeps a row, -1 ends it (no pages, length 0;
+ * the next reserve and step start it over: set its length to -1 to keep it idle).
  * Pages are shared, not copied: reserve copies the ones that a step will write. */
 uaa_status uaa_pages_fork(const uaa_page_args* args, const int32_t* parents,
                           const uaa_workspace* ws, cudaStream_t stream);
@@ -427,7 +430,8 @@ uaa_status uaa_pages_trim(const uaa_page_args* args, int32_t window, int32_t fir
  * that others hold too is replaced, and where it holds rows before the new tokens
  * joined to the moves; if all who hold it ask, the last of them keeps it. All
  * requests are served or none (UAA_DEVFLAG_POOL; counts[2] says how many pages were
- * asked for). A sequence without room for q_len tokens asks for nothing. */
+ * asked for). A sequence without room for q_len tokens, or an idle one (a negative
+ * length), asks for nothing. */
 uaa_status uaa_pages_reserve(const uaa_page_args* args, int32_t q_len, const uaa_workspace* ws,
                              cudaStream_t stream);
 

@@ -311,3 +311,23 @@ def test_lengths_at_the_ends_of_int32(entry, odd):
         assert odd < 0 or flags & B.UAA_DEVFLAG_CAPACITY, (kv, T, page, win)
         if odd < 0 or win:
             assert not got[1].any(), (kv, T, page, win)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("entry", ["step", "split"])
+def test_idle_rows(entry):
+    """A row of negative length: not appended, zero output rows, no flag."""
+    for kv, T, page, win, first in step_cases():
+        a, b, x = step_pair(kv, T, page, win, first, -1)
+
+        def run(layer):
+            if entry == "step":
+                return layer.step(*x, max_seq_len=130, advance_hint=False)
+            layer.append(*x)
+            layer.partial()
+            return layer.combine()
+
+        got = compare_pair(a, b, T, -1, run)
+        assert b.device_status() == 0 and not got[1].any(), (kv, T, page, win)
+    b.set_lengths([-1, -1, -1])
+    assert b.max_len_hint == 0 and not b.step(*x).any() and b.seq_lens.tolist() == [-1] * 3

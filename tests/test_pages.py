@@ -472,3 +472,28 @@ def test_two_layers_on_one_table():
         if int(pages.seq_lens.max()) > P * ps - 45:
             break
     assert step >= 5
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [3, 1500])  # more requests than one pass of the CTA takes
+def test_idle_rows_ask_for_nothing(rows):
+    """A row that ended and is marked idle holds no page and asks for none, through forks
+    of it too; a pool with room for the others alone serves them. At length 0 it
+    starts over."""
+    live = rows // 3
+    pages = table_of([[-1, -1]] * rows, [0] * rows, 16, 2 * live)
+    par = torch.tensor([b if b < live else -1 for b in range(rows)], dtype=torch.int32, device="cuda")
+    pages.fork(par)
+    pages.seq_lens.masked_fill_(par < 0, -1)
+    for step in range(2):
+        pages.reserve(16)
+        assert pages.device_status() == 0 and int(pages.counts[2]) == live
+        pages.seq_lens[:live] += 16
+        pages.trim(40, 1)
+        par = torch.tensor([b if b < live else rows - 1 for b in range(rows)], dtype=torch.int32, device="cuda")
+        pages.fork(par)
+    assert pages.seq_lens.tolist() == [32] * live + [-1] * (rows - live)
+    assert pages.block_table.tolist() == [[b, live + b] for b in range(live)] + [[-1, -1]] * (rows - live)
+    pages.fork(torch.tensor([-1] + list(range(1, rows)), dtype=torch.int32, device="cuda"))
+    pages.reserve(1)
+    assert pages.block_table.tolist()[0] == [0, -1] and pages.device_status() == 0
