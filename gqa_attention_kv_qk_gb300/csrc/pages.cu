@@ -31,14 +31,20 @@ __device__ __forceinline__ void check_entry(const PageParams& p, int e)
     if (e < -1 || e >= p.n_pages) atomicOr(p.status, UAA_DEVFLAG_PAGE);
 }
 
+// A copy that follows finds nothing to do.
+__device__ __forceinline__ void no_moves(const PageParams& p) { p.counts[0] = 0; }
+
 // ---------------------------------------------------------------- fork
 // Row b takes row parents[b] as it was before the call (-1: no pages, length 0).
-// First every new row into the workspace, with the counts; then the rows back.
+// First every new row into the workspace, with the counts; then the rows back. The
+// moves of an operator before this one are void (no_moves): its pages may be others'
+// now.
 __global__ void __launch_bounds__(kPageThreads) fork_gather_kernel(const PageParams p, const int* parents)
 {
     grid_dependency_wait();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kPageThreads + threadIdx.x;
     if (i >= static_cast<int64_t>(p.B) * p.per_seq) return;
+    if (i == 0) no_moves(p);
     const int b = static_cast<int>(i / p.per_seq), l = static_cast<int>(i - static_cast<int64_t>(b) * p.per_seq);
     int par = parents[b];
     if (par < -1 || par >= p.B) {
@@ -72,6 +78,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_small_kernel(const PagePara
 {
     grid_dependency_wait();
     const int n = p.B * p.per_seq;
+    if (threadIdx.x == 0) no_moves(p);
     int now[kForkPer], len[kForkPer];
 #pragma unroll
     for (int k = 0; k < kForkPer; ++k) {
@@ -109,6 +116,7 @@ __global__ void __launch_bounds__(kPageThreads) trim_kernel(const PageParams p, 
     grid_dependency_wait();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kPageThreads + threadIdx.x;
     if (i >= static_cast<int64_t>(p.B) * p.per_seq) return;
+    if (i == 0) no_moves(p);
     const int b = static_cast<int>(i / p.per_seq), l = static_cast<int>(i - static_cast<int64_t>(b) * p.per_seq);
     const int64_t at = static_cast<int64_t>(l) * p.page_size;
     const int e = p.table[i];

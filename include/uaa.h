@@ -443,8 +443,9 @@ uaa_status uaa_pages_compact(const uaa_page_args* args, const uaa_workspace* ws,
 
 /* Copies the pages of the last reserve or compact (counts[0] moves) in every given
  * pool: pool k holds page p in bytes p * page_bytes[k] .. (a multiple of 16). Up to
- * eight pools a call; call it for each layer, once and before the next operator on
- * the table. Moves set up by hand: no page may be the destination of two, or of one
+ * eight pools a call; call it for each layer, once, before the step and the next
+ * operator on the table (fork and trim leave no moves: a copy after them does
+ * nothing). Moves set up by hand: no page may be the destination of two, or of one
  * and the source of another. */
 uaa_status uaa_pages_copy(const uaa_page_args* args, void* const* pools, const int64_t* page_bytes,
                           int32_t n_pools, const uaa_workspace* ws, cudaStream_t stream);

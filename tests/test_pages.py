@@ -497,3 +497,59 @@ def test_idle_rows_ask_for_nothing(rows):
     pages.fork(torch.tensor([-1] + list(range(1, rows)), dtype=torch.int32, device="cuda"))
     pages.reserve(1)
     assert pages.block_table.tolist()[0] == [0, -1] and pages.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [2, 3000])  # fork in one launch, and in two
+@pytest.mark.parametrize("after", ["fork", "trim"])
+def test_copy_after_fork_or_trim_does_nothing(after, rows):
+    """The moves of a reserve are void once the table has changed: a copy that comes too
+    late leaves the pages as the sequences have them now."""
+    pages = table_of([[0, 1, -1]] + [[-1] * 3] * (rows - 1), [20] + [0] * (rows - 1), 16, 8)
+    par = torch.tensor([0, 0] + [-1] * (rows - 2), dtype=torch.int32, device="cuda")
+    pages.fork(par)
+    pages.seq_lens[2:] = -1
+    pages.reserve(1)
+    assert pages.moves[:1].tolist() == [[1, 2]] and int(pages.counts[0]) == 1
+    pool = torch.arange(8, device="cuda", dtype=torch.float32).unsqueeze(1).repeat(1, 64)
+    pages.copy(pool)
+    assert float(pool[2, 0]) == 1.0
+    pool[2] = 50.0                    # the sequence that took page 2 writes it
+    if after == "fork":
+        pages.fork(torch.arange(rows, dtype=torch.int32, device="cuda"))
+    else:
+        pages.trim(100, 0)
+    before = pool.clone()
+    pages.copy(pool)
+    assert torch.equal(pool, before) and int(pages.counts[0]) == 0 and pages.device_status() == 0
+
+
+def marks(pages):
+    """The per-page request marks in the workspace of the page operators."""
+    al = lambda n: (4 * n + 255) // 256 * 256
+    at = 256 + 2 * al(pages.batch * pages.pages_per_seq) + al(pages.batch)
+    return pages.ws_tensor[at:at + 2 * al(pages.n_pages)].view(torch.int32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_len", [(6, 1), (6, 40), (600, 40)])
+def test_requests_leave_no_marks(rows, q_len):
+    """reserve counts who asks for which held page in the workspace, and leaves those
+    counts at zero: after a served call, one in which the last holder keeps its page,
+    and one that the pool could not serve."""
+    table = [[0, 1, 2, -1]] + [[-1] * 4] * (rows - 1)
+    pages = table_of(table, [40] + [0] * (rows - 1), 16, 8 * rows)
+    assert marks(pages).numel() >= 2 * pages.n_pages
+    pages.fork(torch.zeros(rows, dtype=torch.int32, device="cuda"))  # every row holds the same pages
+    for pins in (True, False):
+        if pins:
+            pages.page_refs[3:].add_(1)   # no page is free: refused
+        pages.reserve(q_len if q_len + 40 <= 64 else 20)
+        assert pages.device_status() == (B.UAA_DEVFLAG_POOL if pins else 0)
+        assert not marks(pages).any()
+        if pins:
+            pages.page_refs[3:].sub_(1)
+    assert pages.block_table[-1, 2] == 2  # the last holder kept it
+    assert len(set(pages.block_table[:, 2].tolist())) == rows
+    pages.compact()
+    assert not marks(pages).any() and pages.device_status() == 0
