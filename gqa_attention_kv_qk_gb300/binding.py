@@ -9,8 +9,6 @@ from __future__ import annotations
 import ctypes
 import os
 
-from torch._C import _cuda_getCurrentRawStream as _raw_stream
-
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libuaa.so")
 
 UAA_OK = 0
@@ -330,9 +328,15 @@ def make_desc(cfg: dict) -> UaaAttnDesc:
     return d
 
 
+_raw_stream = None
+
+
 def current_stream(device_index: int) -> int:
     """The raw handle of PyTorch's current stream on a device. (A torch.cuda.Stream
     object costs 3.5 us to make, the launches of a short step not much more.)"""
+    global _raw_stream
+    if _raw_stream is None:  # PyTorch is needed here only: the rest of this module is ctypes
+        from torch._C import _cuda_getCurrentRawStream as _raw_stream
     return _raw_stream(device_index)
 
 

@@ -292,3 +292,21 @@ def test_struct_sizes_match_the_header(L, tmp_path):
             B.UaaStepArgs.q_rot.offset,
             B.UaaWorkspaceLayout.total_bytes.offset, B.UaaAttnDesc.reproducible.offset]
     assert got == want
+
+
+def test_binding_needs_no_pytorch(L):
+    """The host calls (sizes, layouts, refusals) work where PyTorch is missing, or is a
+    build without CUDA."""
+    code = ("import sys, types\n"
+            "sys.modules['torch'] = {torch}\n"
+            "from gqa_attention_kv_qk_gb300 import binding as B\n"
+            "d = B.make_desc(dict(n_q_heads=8, n_kv_heads=2, head_dim=64, rope_style='neox', rope_theta=1e4))\n"
+            "assert B.uaa_workspace_size(d, 2, 100, 152) > 0\n"
+            "assert B.uaa_pages_workspace_size(2, 4, 16) > 0\n"
+            "d.head_dim = 48\n"
+            "assert B.uaa_workspace_size(d, 2, 100, 152) == 0 and 'head_dim=48' in B.last_error()\n")
+    import subprocess
+    import sys
+    for torch_module in ("None", "types.ModuleType('torch')"):
+        r = subprocess.run([sys.executable, "-c", code.format(torch=torch_module)], cwd=ROOT, capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr
