@@ -328,7 +328,19 @@ def make_desc(cfg: dict) -> UaaAttnDesc:
     return d
 
 
-_raw_stream = None
+_raw_stream = _current_device = None
+
+
+def call_stream(stream, device_index: int):
+    """The stream a call on tensors of this device runs on: the given one, or PyTorch's
+    current one. The library launches on the current device, so another one refuses."""
+    global _current_device
+    if _current_device is None:
+        from torch._C import _cuda_getDevice as _current_device
+    if _current_device() != device_index:
+        raise RuntimeError(f"the tensors are on cuda:{device_index}, and the current device is "
+                           f"cuda:{_current_device()}: make the call under torch.cuda.device({device_index})")
+    return current_stream(device_index) if stream is None else stream
 
 
 def current_stream(device_index: int) -> int:

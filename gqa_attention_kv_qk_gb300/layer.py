@@ -173,7 +173,7 @@ class DecodeLayer:
         holds fp32 values, and for a q8 or q4 layer `k` too, quantised on the device by
         uaa_vq8_quantize or uaa_q4_quantize (the append's own rules)."""
         D = self.cfg["head_dim"]
-        s = torch.cuda.current_stream(self.device)
+        s = B.call_stream(None, self._index)
 
         def put(vals, cache, scales):
             if scales is not None:  # codes and scales of the logical rows, then into place
@@ -275,7 +275,7 @@ class DecodeLayer:
         max_seq_len: a bound on the lengths before the step, for a capture or where the
         caller knows one (default: the layer's own, read from the device when the
         capacity would end by it)."""
-        s = stream if stream is not None else B.current_stream(self._index)
+        s = B.call_stream(stream, self._index)
         T = self._begin(q, stream)
         want = self.out_for(T)
         if out is not None:
@@ -295,7 +295,7 @@ class DecodeLayer:
         others), overwritten by the next read of n rows, as a step's output is by the
         next step; work on another stream than the read's waits for it, and keeps them
         (record_stream) for as long as it uses them."""
-        s = stream if stream is not None else B.current_stream(self._index)
+        s = B.call_stream(stream, self._index)
         if start is not None and (start.dtype is not torch.int32 or start.shape != self.seq_lens.shape
                                   or start.get_device() != self._index or not start.is_contiguous()):
             raise ValueError("start is not a contiguous int32 tensor [batch] on the device")
@@ -312,23 +312,23 @@ class DecodeLayer:
         return got
 
     def append(self, q, k_new, v_new, stream=None, q_rot=None):
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        s = B.call_stream(stream, self._index)
         self._bound(self._begin(q, stream), stream)
         B.uaa_rope_qk_norm_append(self.desc, self.args(q, k_new, v_new, q_rot=q_rot), self.ws, s)
 
     def append_partial(self, q, k_new, v_new, stream=None, q_rot=None):
         """Steps 1 and 2 (one fused kernel for bf16 / vq8 / q8 caches and one token);
         follow with combine()."""
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        s = B.call_stream(stream, self._index)
         self._bound(self._begin(q, stream), stream)
         B.uaa_decode_attn_append_partial(self.desc, self.args(q, k_new, v_new, q_rot=q_rot), self.ws, s)
 
     def partial(self, stream=None):
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        s = B.call_stream(stream, self._index)
         B.uaa_decode_attn_partial(self.desc, self.args(None, None, None), self.ws, s)
 
     def combine(self, stream=None):
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        s = B.call_stream(stream, self._index)
         B.uaa_decode_attn_combine(self.desc, self.args(None, None, None), self.ws, s)
         self.max_len_hint += self.q_len
         return self.out_for(self.q_len)
@@ -338,5 +338,5 @@ class DecodeLayer:
                                           self.max_len_hint if max_seq_len is None else max_seq_len, 0, self.q_len)
 
     def device_status(self, stream=None) -> int:
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        s = B.call_stream(stream, self._index)
         return B.uaa_device_status(self.ws, s)

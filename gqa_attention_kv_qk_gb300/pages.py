@@ -68,7 +68,7 @@ class PageTable:
         a.moves, a.counts = B.ptr(self.moves), B.ptr(self.counts)
 
     def _s(self, stream):
-        return stream if stream is not None else B.current_stream(self.device.index)
+        return B.call_stream(stream, self.device.index)
 
     def fork(self, parents, stream=None):
         """Row b becomes a copy of row parents[b] (int32 [batch] on the device; -1: it ends)."""

@@ -110,7 +110,7 @@ def test_new_tensors_belong_to_the_stream_that_writes_them(monkeypatch):
     monkeypatch.setattr(torch, "empty", recorded)
     monkeypatch.setattr(B, "uaa_cache_read", lambda *a, **k: 0)
     monkeypatch.setattr(B, "uaa_decode_attn", lambda *a, **k: 0)
-    monkeypatch.setattr(B, "current_stream", lambda index: 7)
+    monkeypatch.setattr(B, "call_stream", lambda stream, index: stream or 7)
     layer = L.DecodeLayer.__new__(L.DecodeLayer)
     layer.cfg, layer.batch, layer.max_q_len, layer._index, layer.device = config(), 1, 4, 0, torch.device("cpu")
     layer.out, layer._reads, layer._read_args, layer.seq_lens = empty(1, 4, 64), {}, object(), torch.zeros(1)
@@ -168,8 +168,7 @@ def test_length_bound_on_the_host(monkeypatch):
     passed, capturing = [], [False]
     monkeypatch.setattr(B, "uaa_decode_attn", lambda *a, **k: 0)
     monkeypatch.setattr(B, "uaa_rope_qk_norm_append", lambda *a, **k: 0)
-    monkeypatch.setattr(B, "current_stream", lambda index: 7)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: 7)
+    monkeypatch.setattr(B, "call_stream", lambda stream, index: stream or 7)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
     layer = L.DecodeLayer.__new__(L.DecodeLayer)
     layer.batch, layer.capacity, layer.max_q_len, layer._index, layer.device = 2, 64, 7, 0, torch.device("cpu")
@@ -331,3 +330,48 @@ def test_idle_rows(entry):
         assert b.device_status() == 0 and not got[1].any(), (kv, T, page, win)
     b.set_lengths([-1, -1, -1])
     assert b.max_len_hint == 0 and not b.step(*x).any() and b.seq_lens.tolist() == [-1] * 3
+
+
+# ---------------------------------------------------------------- another current device
+
+def test_calls_of_another_device_are_refused(monkeypatch):
+    """The library launches on the current device: a layer or table of another one says so
+    before anything is launched, with its own stream or with a given one."""
+    from gqa_attention_kv_qk_gb300 import layer as L
+    from gqa_attention_kv_qk_gb300 import pages as P
+    import gqa_attention_kv_qk_gb300.binding as binding
+
+    def launched(*a, **k):
+        raise AssertionError("a launch on the wrong device")
+
+    for name in vars(binding).copy():
+        if name.startswith("uaa_"):
+            monkeypatch.setattr(binding, name, launched)
+    monkeypatch.setattr(binding, "_current_device", lambda: 0)
+    monkeypatch.setattr(binding, "_raw_stream", lambda index: 0)
+    layer = L.DecodeLayer.__new__(L.DecodeLayer)
+    layer.cfg, layer.batch, layer.max_q_len, layer._index, layer.device = config(), 1, 4, 1, torch.device("cuda", 1)
+    layer.seq_lens, layer.capacity, layer.max_len_hint, layer.q_len = torch.zeros(1), 64, 0, 1
+    layer.out = torch.empty(1, 4, 64)
+    layer._outs, layer.args, layer.desc, layer.ws = {1: layer.out}, lambda *a, **k: None, None, None
+    layer._reads, layer._read_args, layer._args = {1: (layer.out, layer.out)}, object(), lambda *a: None
+    table = P.PageTable.__new__(P.PageTable)
+    table.device, table.args, table.ws, table.n_pages = torch.device("cuda", 1), None, None, 4
+
+    class Parents:
+        dtype, shape = torch.int32, table.__dict__.setdefault("seq_lens", torch.zeros(1)).shape
+        get_device, is_contiguous, data_ptr = (lambda s: 1), (lambda s: True), (lambda s: 0)
+
+    q = torch.zeros(1, 4, 64)
+    for stream in (None, 0x77):
+        for call in (lambda: layer.step(q, q, q, stream=stream), lambda: layer.append(q, q, q, stream=stream),
+                     lambda: layer.append_partial(q, q, q, stream=stream), lambda: layer.partial(stream=stream),
+                     lambda: layer.combine(stream=stream), lambda: layer.read_rows(None, 1, stream=stream),
+                     lambda: layer.device_status(stream=stream), lambda: table.fork(Parents(), stream=stream),
+                     lambda: table.trim(3, stream=stream), lambda: table.reserve(stream=stream),
+                     lambda: table.compact(stream=stream), lambda: table.copy(stream=stream),
+                     lambda: table.device_status(stream=stream)):
+            with pytest.raises(RuntimeError, match="on cuda:1, and the current device is cuda:0"):
+                call()
+    layer._index = 0
+    assert binding.call_stream(None, 0) == 0 and binding.call_stream(0x77, 0) == 0x77
