@@ -44,10 +44,13 @@ class DecodeLayer:
     sequence one step takes (q, k_new, v_new of shape [B][T][H][D]); the
     workspace is sized for it. cache: the caller's own tensors for some of k_cache,
     v_cache, k_scale, v_scale and seq_lens (a pool shared with other layers, a cache
-    filled before), used in place instead of new ones."""
+    filled before), used in place instead of new ones. workspace: a uint8 tensor of
+    B.uaa_workspace_size bytes and more, zeroed once, or another layer's ws_tensor:
+    layers whose steps run one after another share one (prefill chunks over a 4-bit
+    cache take up to 512 MiB of it, or the widened rows of one sequence)."""
 
     def __init__(self, cfg: dict, batch: int, capacity: int, device="cuda", page_size=None, block_table=None,
-                 n_pages=None, max_q_len=1, cache=None):
+                 n_pages=None, max_q_len=1, cache=None, workspace=None):
         self.cfg = dict(cfg)
         self.device = _require_cuda(device)
         self._index = self.device.index
@@ -108,8 +111,12 @@ class DecodeLayer:
         nbytes = B.uaa_workspace_size(self.desc, batch, capacity - 1, 0, self.max_q_len)
         if nbytes == 0:
             raise B.UaaError(B.UAA_ERR_UNSUPPORTED, B.last_error())
-        self.ws_tensor = torch.zeros((nbytes,), dtype=torch.uint8, device=dev)
-        self.ws = B.UaaWorkspace(self.ws_tensor.data_ptr(), nbytes)
+        w = torch.zeros((nbytes,), dtype=torch.uint8, device=dev) if workspace is None else workspace
+        if w.dtype != torch.uint8 or w.dim() != 1 or not w.is_contiguous() or w.device != dev or w.numel() < nbytes:
+            raise ValueError(f"workspace is {tuple(w.shape)} {w.dtype} on {w.device}, the layer needs {nbytes} "
+                             f"contiguous bytes (uint8) on its device")
+        self.ws_tensor = w
+        self.ws = B.UaaWorkspace(w.data_ptr(), w.numel())
 
     @classmethod
     def for_case(cls, case: dict, device="cuda") -> "DecodeLayer":

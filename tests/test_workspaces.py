@@ -132,3 +132,34 @@ def test_shorter_steps_than_the_longest(heads, kv_heads, longest):
         err = (out.double().cpu().reshape(want.shape) - want).abs()
         assert float(err.max()) <= 4e-3 and float(err.mean()) <= 4e-4, T
         n += T
+
+
+@pytest.mark.gpu
+def test_layers_that_share_a_workspace():
+    """Layers of every kind on one workspace, one step after another (single tokens,
+    drafts and prefill chunks), give what they give on workspaces of their own."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    kinds = [dict(kv_dtype=kv, io_dtype="f32" if kv == "f32" else "bf16", head_dim=D, reproducible=True, **kw)
+             for kv, D, kw in (("q4", 128, {}), ("f32", 64, {}), ("q4", 64, dict(window=90, first_tokens=5)),
+                               ("bf16", 128, {}), ("q8", 256, {}), ("vq8", 64, {}))]
+    cfgs = [config(n_q_heads=16, n_kv_heads=4, **k) for k in kinds]
+    batch, cap, longest = 3, 1024, 40
+    need = [B.uaa_workspace_size(B.make_desc(c), batch, cap - 1, 0, longest) for c in cfgs]
+    shared = torch.zeros(max(need), dtype=torch.uint8, device="cuda")
+    own = [DecodeLayer(c, batch, cap, max_q_len=longest) for c in cfgs]
+    one = [DecodeLayer(c, batch, cap, max_q_len=longest, workspace=shared) for c in cfgs]
+    assert all(x.ws_tensor is shared for x in one) and own[0].ws_tensor.numel() == need[0]
+    assert DecodeLayer(cfgs[0], batch, cap, max_q_len=longest, workspace=own[0].ws_tensor).ws.bytes == need[0]
+    for i, T in enumerate((40, 1, 3, 1, 1, 40, *[1] * 3, 40, 40, 40, 40, 40, 40, 40, 40, 40, 40, 40, 40, 1, 4, 1)):
+        for a, b, cfg in zip(own, one, cfgs):
+            x = rows(cfg, batch, T, i)
+            assert torch.equal(a.step(*x), b.step(*x)), (cfg["kv_dtype"], i, T)
+    for a, b in zip(own, one):
+        assert torch.equal(a.k_cache, b.k_cache) and torch.equal(a.seq_lens, b.seq_lens)
+        assert a.device_status() == 0 and b.device_status() == 0
+    for bad in (shared[:need[0] - 1], shared.view(torch.int8), shared.cpu(), shared.repeat(2)[::2], shared.view(-1, 2)):
+        with pytest.raises(ValueError, match="workspace"):
+            DecodeLayer(cfgs[0], batch, cap, max_q_len=longest, workspace=bad)
+    with pytest.raises(B.UaaError, match="16-byte aligned"):
+        layer = DecodeLayer(cfgs[5], batch, cap, workspace=shared[8:])
+        layer.step(*rows(cfgs[5], batch, 1, 0))
