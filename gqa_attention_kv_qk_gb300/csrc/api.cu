@@ -382,14 +382,33 @@ uaa_status check_args(const uaa_attn_desc* d, const uaa_step_args* a, const uaa_
     return UAA_OK;
 }
 
+// The partial kernels count a slice's key stages over all its units in 32 bits.
+uaa_status check_stages(const uaa_attn_desc* d, const uaa_step_args* a, const Plan& pl)
+{
+    if (pl.prefill && (!a->block_table || pl.dense_rows > 0)) return UAA_OK;  // not theirs (takes_prefill)
+    long long keys = (long long)a->max_seq_len + pl.q_len;
+    if (d->window > 0) {  // two runs, each with a stage more where it starts inside one
+        const long long seen = (long long)d->window + pl.q_len - 1 + d->first_tokens;
+        keys = keys < seen ? keys : seen;
+    }
+    const long long stages = keys / (uaa::kTileKeys * pl.mg) + 3;
+    const double all = (double)stages * pl.slice * d->n_kv_heads * pl.head_groups;
+    if (a->batch > 0 && all > 2147483647.0)
+        return fail(UAA_ERR_UNSUPPORTED,
+                    "max_seq_len=%d, q_len=%d: %.3g key stages over %d sequences exceed 2^31 (split the batch or the tokens)",
+                    a->max_seq_len, pl.q_len, all, pl.slice);
+    return UAA_OK;
+}
+
 uaa_status prepare(const uaa_attn_desc* d, const uaa_step_args* a, const uaa_workspace* ws, bool need_io,
                    Plan* pl)
 {
     UAA_TRY(check_desc(d));
     UAA_TRY(check_args(d, a, ws, need_io));
     const int n_sm = device_sm_count();
+    UAA_TRY(make_plan(d, a->batch, a->q_len, a->max_seq_len, n_sm > 0 ? n_sm : 1, pl));
+    UAA_TRY(check_stages(d, a, *pl));
     if (n_sm <= 0) return fail(UAA_ERR_CUDA, "no CUDA device: the SM count query failed");
-    UAA_TRY(make_plan(d, a->batch, a->q_len, a->max_seq_len, n_sm, pl));
     if (ws->bytes < pl->total)
         return fail(UAA_ERR_INVALID_ARGUMENT, "workspace has %zu bytes, the step needs %zu", ws->bytes,
                     pl->total);
@@ -1383,6 +1402,7 @@ extern "C" uaa_status uaa_decode_attn_static(const uaa_attn_desc* desc, const ua
     UAA_TRY(static_scratch_address(&scratch));
     const uaa_workspace ws{scratch, (size_t)UAA_STATIC_SCRATCH_BYTES};
     UAA_TRY(check_args(desc, args, &ws, true));
+    UAA_TRY(check_stages(desc, args, pl));
     if (args->batch == 0) return UAA_OK;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -310,3 +310,24 @@ def test_binding_needs_no_pytorch(L):
     for torch_module in ("None", "types.ModuleType('torch')"):
         r = subprocess.run([sys.executable, "-c", code.format(torch=torch_module)], cwd=ROOT, capture_output=True, text=True)
         assert r.returncode == 0, r.stderr
+
+
+def test_steps_beyond_2_31_stages_are_refused(L):
+    """A slice's key stages over all its units are counted in 32 bits: 1,024 sequences of
+    2^20 positions, 1,024 tokens each, have 3.4e10 of them. (A paged table: no cache of
+    that many positions is needed for it.) The window's keys alone fit."""
+    big = dict(batch=1024, cache_capacity=2**20, max_seq_len=2**20 - 1024, q_len=1024, block_table=0x10000, page_size=64,
+               pages_per_seq=2**14, n_pages=16)
+    for over in (dict(), dict(kv_dtype="q8"), dict(kv_dtype="f32"), dict(kv_dtype="q4", head_dim=256),
+                 dict(window=2**19, first_tokens=5)):
+        d = good_desc(n_q_heads=64, n_kv_heads=8, **over)
+        for call in (B.uaa_decode_attn, B.uaa_decode_attn_append_partial, B.uaa_decode_attn_partial):
+            assert call(d, fake_args(k_scale=0x10000, **big), WS, None, check=False) == B.UAA_ERR_UNSUPPORTED, over
+            assert "key stages over 1024 sequences exceed 2^31" in B.last_error()
+    # not refused for their stages (there is no device here, or the workspace is too small)
+    for d, kw in ((good_desc(n_q_heads=64, n_kv_heads=8, window=2000, first_tokens=5), big),
+                  (good_desc(n_q_heads=64, n_kv_heads=8), dict(big, max_seq_len=1000)),
+                  (good_desc(n_q_heads=64, n_kv_heads=8, kv_dtype="q4"), big)):  # a prefill chunk's own kernel
+        tiny = B.UaaWorkspace(0x20000, 256)
+        st = B.uaa_decode_attn(d, fake_args(k_scale=0x10000, **{**big, **kw}), tiny, None, check=False)
+        assert st in (B.UAA_ERR_CUDA, B.UAA_ERR_INVALID_ARGUMENT) and "stages" not in B.last_error()
