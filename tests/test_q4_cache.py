@@ -541,3 +541,27 @@ def test_long_tail_behind_a_dominant_key(kind):
         assert 0.9 * (n + t) * 2.0 ** -24.8 < r < 1.1 * (n + t) * 2.0 ** -24.7
         got = out.double().cpu().reshape(Bn, T, Hkv, 64)[:, t]
         assert float((got - want).abs().max()) <= 7 * r * 2.0 ** -11 * 19.2, (t, want, float(got.min()), float(got.max()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,page,D", [(1, 0, 64), (1, 32, 128), (3, 0, 64), (3, 32, 64), (64, 0, 64)])
+def test_batches_of_more_than_one_slice(T, page, D):
+    """1,030 sequences: two launches of the split-K kernel, with sequences of the second
+    one at every place of a window with first tokens."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    n = 1030
+    lens = [(7 * b) % 90 for b in range(n)]
+    cfg = config(n_q_heads=2, n_kv_heads=1, head_dim=D, batch=n, seq_len=90, q_len=T, page_size=page, window=20,
+                 first_tokens=3)
+    case = W.host_case(cfg, lens=lens)
+    layer = DecodeLayer.for_case(case)
+    assert layer.layout().n_slices == 2
+    q_rot = torch.empty((n, T, 2, D), device="cuda")
+    out = layer.step(*(case[k].cuda() for k in ("q", "k_new", "v_new")), q_rot=q_rot)
+    torch.cuda.synchronize()
+    assert layer.device_status() == 0 and layer.seq_lens.tolist() == [x + T for x in lens]
+    k, v = plain64.cached_values(layer)
+    some = sorted({*range(0, n, 37), *range(1015, 1030)})
+    want = plain64.attend(q_rot[some], k[some], v[some], [lens[b] for b in some], 20, 3)
+    err = (out.double().cpu().reshape(n, T, 2, D)[some] - want).abs()
+    assert float(err.max()) <= TOL_MAX and float(err.mean()) <= TOL_MEAN
