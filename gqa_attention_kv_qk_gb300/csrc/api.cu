@@ -126,7 +126,7 @@ struct Plan {
     int slice;           // sequences per partial launch
     int n_slices;
     int per_sm;          // resident CTAs per SM
-    int prefill;         // a contiguous cache takes the query-tiled prefill kernel (no combine)
+    int prefill;         // a contiguous or 4-bit cache takes the query-tiled prefill kernel (no combine)
     int dense_rows;      // 4-bit caches there: rows per (sequence, kv head) widened in the workspace,
     int dense_batch;     // for so many sequences at a time (0 rows: other caches)
     size_t off_status, off_counts, off_qrot, off_prefix, off_rec_lse, off_rec_o, off_ranges, off_owners, off_balance, off_dense, total;
@@ -205,8 +205,9 @@ uaa_status make_plan(const uaa_attn_desc* d, int batch, int q_len, int max_len, 
     p.mg = p.kernel == 1 ? uaa::partial_tc_keys_per_stage(d->head_dim, d->kv_dtype, p.n_head_tiles) / uaa::kTileKeys : 1;
     p.per_sm = p.kernel == 0 ? 4 : uaa::partial_tc_ctas_per_sm(d->head_dim, d->kv_dtype, p.n_head_tiles);
     p.n_ctas = n_sm * p.per_sm;
-    // long chunks on contiguous bf16 caches: whole 64-row blocks of (token, head) rows
-    // per CTA, each streaming its keys once (the partial kernel's units hold 16 rows)
+    // long chunks on contiguous bf16 caches and on 4-bit caches: whole 128-row blocks of
+    // (token, head) rows per CTA, each streaming its keys once (the partial kernel's units
+    // hold 8 to 24 rows)
     p.prefill = p.kernel == 1 && (d->kv_dtype == UAA_DTYPE_BF16 || d->kv_dtype == UAA_DTYPE_Q4) &&
                 (d->head_dim == 64 || d->head_dim == 128) && rows >= uaa::kPrefillRows;
     p.slice = batch < uaa::kMaxSliceBatch ? (batch > 0 ? batch : 1) : uaa::kMaxSliceBatch;

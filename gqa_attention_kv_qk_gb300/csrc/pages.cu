@@ -330,9 +330,9 @@ __global__ void __launch_bounds__(kScanThreads) reserve_kernel(const PageParams 
     const bool enough = found >= takes;
 
     // the new entries, and the pages to copy (those with rows before the new tokens).
-    // A request's decision reads counts that others change here: a round's threads
-    // decide, meet, and then apply; a page's count only falls by requests that take
-    // another page, so stays() is decided from the counts kept in table_tmp.
+    // stays() reads counts and marks of held pages, which nothing changes in this loop:
+    // the counts set here are those of free pages, and the pages given up are listed in
+    // table_tmp and taken off their counts after it.
     int given = 0, copies = 0;
     for (int64_t i0 = 0; i0 < n_req; i0 += kScanThreads) {
         const Request r = request_of(p, i0 + tid, per, q_len);

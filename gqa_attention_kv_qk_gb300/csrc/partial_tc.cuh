@@ -1,4 +1,4 @@
-// partial_tc.cuh -- split-K decode partial for bf16, vq8 and q8 caches: a persistent,
+// partial_tc.cuh -- split-K decode partial for bf16, vq8, q8 and 4-bit caches: a persistent,
 // warp-specialised kernel with TMA tile loads into a shared-memory ring and
 // tensor-core contractions.
 //
@@ -11,7 +11,8 @@
 // step (steps 1 and 2 in one launch); otherwise it reads the q' rows that the
 // separate append left in the workspace.
 //
-// Warp roles (192 threads):
+// Warp roles (192 threads; 320 with eight consumer warps, for units of two 8-row
+// tiles, where the producer and prep warps are 8 and 9):
 //   warp 5 (prep): walks the same segments one ahead of the consumers and
 //     writes each segment's q' rows, as bf16 hi + lo fragments, into a shared
 //     slot: fused, it normalises, rotates and prescales the unit's q rows
@@ -24,6 +25,7 @@
 //     stages, TK = 64 MG keys each, with 2-D TMA loads (cp.async.bulk.tensor)
 //     into a ring of kStages stages, straight across segment boundaries. bf16
 //     key and value boxes are TK rows x 128 bytes with the 128-byte swizzle;
+//     4-bit code boxes TK rows x D / 2 bytes (consume_q4 has their arithmetic);
 //     int8 code boxes (vq8 / q8 values, q8 keys) are TK rows x min(D, 128) bytes
 //     with the 64- or 128-byte swizzle; scales are one TK-float box per row
 //     kind. Full / empty mbarriers pass
@@ -252,7 +254,10 @@ __device__ __forceinline__ void widen_code_quad(uint32_t r, uint32_t& d01, uint3
     d23 = hsub2_u32(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
 }
 
-// 4-bit codes, u = code + 8. A register r holds nibbles 0-3 of two 16-bit halves.
+// 4-bit codes, u = code + 8. (An integer or-ed into the mantissa of a float whose last
+// bits count in its unit, and the float's own value taken off: the magic-number
+// conversion of integers, a published technique.) A register r holds nibbles 0-3 of two
+// 16-bit halves.
 // Nibble 0 of both halves becomes the fp16 pair 1024 + u (mantissa bits 0-3 of
 // 0x6400), nibble 1 the pair 64 + u (bits 4-7 of 0x5400); r >> 8 gives nibbles 2
 // and 3 the same way. So four pairs take one shift and four and-ors of the integer

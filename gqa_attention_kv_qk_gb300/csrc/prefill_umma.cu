@@ -25,7 +25,8 @@
 //   softmax: four threads own row r (TMEM lane r), one per 32-key quarter: they
 //     read S_j, apply softcap and the causal / window masks, and keep a
 //     running maximum m that they raise only when a logit exceeds it by more
-//     than 2^8 (exp2(s - m) <= 256 otherwise; the final division cancels m),
+//     than 2^8 (exp2(s - m) <= 256 otherwise, 2^15 with F16, whose m lies 7 lower;
+//     the final division cancels m),
 //     rescaling the O row in TMEM then; P_j = exp2(S_j - m) goes back to TMEM
 //     as bf16 hi + lo parts (by truncation: 2^-14 relative);
 //   O (128 x D, fp32 in TMEM) += P_j . V_j, P_j the MMA's A operand in TMEM,

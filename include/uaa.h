@@ -107,7 +107,9 @@ typedef enum {
  * Q4: keys and values as 4-bit codes, each group of 32 dims with its own fp16 scale
  * (the rule of uaa_q4_quantize): a row is D / 2 bytes of codes and D / 32 scales.
  * k_cache / v_cache then hold the codes ([..][D / 2] bytes), and k_scale / v_scale
- * address the scales ([..][D / 32] fp16, cast to float*). |q'| as with Q8. */
+ * address the scales ([..][D / 32] fp16, cast to float*). |q'| as with Q8. q' and
+ * the softmax weights enter the tensor core as one fp16 part each (2^-11 relative;
+ * the other kinds take two parts, 2^-16), against keys and values of 4 bits. */
 typedef enum {
     UAA_DTYPE_F32 = 0,
     UAA_DTYPE_BF16 = 1,
@@ -231,10 +233,11 @@ typedef struct {
 /* Scratch memory owned by the caller, at least uaa_workspace_size bytes, zeroed
  * once after allocation. It holds the rotated q rows, the split partials, the
  * device status word, the arrival counter of the append and fused kernels (the
- * last CTA to arrive advances seq_lens) and the range
- * balance state (counters that every completed launch leaves at zero, and the
- * measured slot speeds that carry over to the next launch); it must not be
- * shared by steps that run concurrently. After UAA_DEVFLAG_TIMEOUT zero it
+ * last CTA to arrive advances seq_lens), the range balance state (the measured
+ * slot speeds carry over to the next launch) and the fp32 step's split counters;
+ * every completed launch leaves the counters at zero. It must not be shared by
+ * steps that run concurrently, and may be by layers whose steps run one after
+ * another. After UAA_DEVFLAG_TIMEOUT zero it
  * again. A workspace may serve descs of different geometry in turn (different
  * P = uaa_workspace_layout.n_ctas); the measured slot speeds then start over
  * at each change of P (uniform ranges for one launch). */
@@ -296,12 +299,13 @@ uaa_status uaa_rope_qk_norm_append(const uaa_attn_desc* desc, const uaa_step_arg
  * (token, head) rows per kv head; uaa_workspace_layout.kernel == 2) takes the
  * query-tiled prefill kernel instead: a CTA per (sequence, kv head, block of
  * 128 rows) reads each key and value tile its rows see once, and writes the
- * block's output rows itself (sink included); rows of a sequence the append
- * could not take are zero. Step 3 then has nothing to do. A 4-bit cache, paged or
- * not, takes it too, over its visible rows widened to fp16 in the workspace (up to
- * 512 MiB of it, some sequences at a time); there a sequence beyond
- * max_seq_len (UAA_DEVFLAG_LEN_HINT) has no room in the workspace and gets zero
- * rows. */
+ * block's output rows itself (sink included). Step 3 then has nothing to do. A
+ * 4-bit cache, paged or not, takes it too, over its visible rows widened to fp16 in
+ * the workspace (up to 512 MiB of it, some sequences at a time; more only where one
+ * sequence of max_seq_len + q_len positions needs it, window or not); there a
+ * sequence beyond max_seq_len (UAA_DEVFLAG_LEN_HINT) has no room in the workspace
+ * and gets zero rows. The output rows of a sequence that the append could not take
+ * (UAA_DEVFLAG_CAPACITY) mean nothing; those of an idle row are zero. */
 uaa_status uaa_decode_attn_partial(const uaa_attn_desc* desc, const uaa_step_args* args,
                                    const uaa_workspace* ws, cudaStream_t stream);
 
@@ -319,8 +323,9 @@ uaa_status uaa_decode_attn_combine(const uaa_attn_desc* desc, const uaa_step_arg
  * those of uaa_rope_qk_norm_append followed by uaa_decode_attn_partial, up to
  * fp32 rounding order (bf16 key rows in the cache are the same bits; the step's
  * own attention may use a new key element one bf16 ulp away where its exact
- * rounding is recomputed after the attention; a q8 key code may differ by one
- * where the rotated key lies within fp32 rounding of a rounding tie). For fp32 caches,
+ * rounding is recomputed after the attention; a q8 or q4 key code may differ by one,
+ * and a scale by a rounding step, where the rotated key lies within fp32 rounding of
+ * a rounding tie). For fp32 caches,
  * and for steps of q_len > 1, it is those two launches. Follow it with
  * uaa_decode_attn_combine. */
 uaa_status uaa_decode_attn_append_partial(const uaa_attn_desc* desc, const uaa_step_args* args,
