@@ -331,24 +331,29 @@ def make_desc(cfg: dict) -> UaaAttnDesc:
 _raw_stream = _current_device = None
 
 
+def _bind_streams():
+    """PyTorch is needed here only: the rest of this module is ctypes."""
+    global _raw_stream, _current_device
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream, _cuda_getDevice as _current_device
+
+
 def call_stream(stream, device_index: int):
     """The stream a call on tensors of this device runs on: the given one, or PyTorch's
-    current one. The library launches on the current device, so another one refuses."""
-    global _current_device
+    current one as a raw handle. (A torch.cuda.Stream object costs 3.5 us to make, the
+    launches of a short step not much more.) The library launches on the current
+    device, so another one refuses."""
     if _current_device is None:
-        from torch._C import _cuda_getDevice as _current_device
+        _bind_streams()
     if _current_device() != device_index:
         raise RuntimeError(f"the tensors are on cuda:{device_index}, and the current device is "
                            f"cuda:{_current_device()}: make the call under torch.cuda.device({device_index})")
-    return current_stream(device_index) if stream is None else stream
+    return _raw_stream(device_index) if stream is None else stream
 
 
 def current_stream(device_index: int) -> int:
-    """The raw handle of PyTorch's current stream on a device. (A torch.cuda.Stream
-    object costs 3.5 us to make, the launches of a short step not much more.)"""
-    global _raw_stream
-    if _raw_stream is None:  # PyTorch is needed here only: the rest of this module is ctypes
-        from torch._C import _cuda_getCurrentRawStream as _raw_stream
+    """The raw handle of PyTorch's current stream on a device."""
+    if _raw_stream is None:
+        _bind_streams()
     return _raw_stream(device_index)
 
 

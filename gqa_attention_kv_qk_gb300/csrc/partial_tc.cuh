@@ -48,10 +48,10 @@
 //       is then a pair of adjacent codes), one byte permute and one fp16
 //       subtract per pair widen the codes exactly, and the PV product runs in
 //       fp16. The per-key scale is folded into P; to keep P * scale inside
-//       [0, 2^14] it is divided by the warp's running maximum scale r and taken
-//       2^14 times, and O is kept in units of r 2^-14 (a new maximum rescales O as
-//       a new logit maximum does). (In [0, 1] fp16's smallest step, 2^-24, rounded
-//       away a long tail of keys behind a dominant one.)
+//       [0, 2^14] it is divided by the warp's running maximum scale times 2^-14, r,
+//       and O is kept in units of r (a new maximum rescales O as a new logit maximum
+//       does). (In [0, 1] fp16's smallest step, 2^-24, rounded away a long tail of
+//       keys behind a dominant one.)
 //     The warp that owns the new key's row copies the staged rows over that
 //     row of the unit's last stage after it lands (the tile load brought
 //     whatever the slot held before the step).
@@ -1434,7 +1434,9 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
             for (int mi = 0; mi < KS; ++mi) o[nt][mi][0] = o[nt][mi][1] = o[nt][mi][2] = o[nt][mi][3] = 0.f;
         }
-        float r_scale = 0.f;  // vq8: the warp's running maximum value scale (O is kept in units of it / kPScale)
+        // vq8: the warp's running maximum value scale / kPScale (O is kept in units of it);
+        // never 0, so that its reciprocal needs no care
+        float r_scale = 1.175494351e-38f;
 
         for (int k = 0; k < sg.n_st; ++k, ++it) {
             const int s = it % SH::kStages;
@@ -1563,13 +1565,13 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     }
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, off));
-                    const float r_new = fmaxf(r_scale, smax);
-                    const float inv = r_new > 0.f ? ptx::rcp(r_new) : 0.f;
-                    r_ratio = r_new > 0.f ? r_scale * inv : 1.f;
+                    const float r_new = fmaxf(r_scale, smax * (1.f / kPScale));
+                    const float inv = ptx::rcp(r_new);
+                    r_ratio = r_scale * inv;
 #pragma unroll
                     for (int mg = 0; mg < MG; ++mg) {
-                        w_g[mg] *= inv * kPScale;
-                        w_g8[mg] *= inv * kPScale;
+                        w_g[mg] *= inv;
+                        w_g8[mg] *= inv;
                     }
                     r_scale = r_new;
                 }
@@ -1746,8 +1748,7 @@ partial_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         const int hc = (nt0 + nt) * 8 + 2 * t + (e & 1);
                         const int d = Q4 ? 32 * (mi >> 1) + 4 * g + 2 * (mi & 1) + (e >> 1)
                                     : VQ8 ? 16 * mi + 2 * g + (e >> 1) : 16 * mi + g + 8 * (e >> 1);
-                        if (d >= c0 && d < c0 + RC) red_o[(kgrp * HC + hc) * (RC + 4) + d - c0] =
-                            VQ8 ? o[nt][mi][e] * (1.f / kPScale) * o_unit : o[nt][mi][e];
+                        if (d >= c0 && d < c0 + RC) red_o[(kgrp * HC + hc) * (RC + 4) + d - c0] = o[nt][mi][e] * o_unit;
                     }
             ptx::named_barrier_sync(1, CW * 32);
             for (int idx = threadIdx.x; idx < nh * RC; idx += CW * 32) {

@@ -39,6 +39,7 @@ class PageTable:
         dev = torch.device(device)
         self.device = dev = dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
         to = lambda t: torch.as_tensor(t, dtype=torch.int32).to(dev).contiguous()
+        self._index = dev.index
         self.block_table = to(block_table)
         if self.block_table.dim() != 2:
             raise ValueError(f"block_table has {self.block_table.dim()} dimensions, not 2")
@@ -68,12 +69,12 @@ class PageTable:
         a.moves, a.counts = B.ptr(self.moves), B.ptr(self.counts)
 
     def _s(self, stream):
-        return B.call_stream(stream, self.device.index)
+        return B.call_stream(stream, self._index)
 
     def fork(self, parents, stream=None):
         """Row b becomes a copy of row parents[b] (int32 [batch] on the device; -1: it ends)."""
         if (parents.dtype is not torch.int32 or parents.shape != self.seq_lens.shape
-                or parents.get_device() != self.device.index or not parents.is_contiguous()):
+                or parents.get_device() != self._index or not parents.is_contiguous()):
             raise ValueError("parents is not a contiguous int32 tensor [batch] on the device")
         B.uaa_pages_fork(self.args, B.ptr(parents), self.ws, self._s(stream))
 
@@ -93,7 +94,7 @@ class PageTable:
         """The copies of the last reserve() or compact() in pools [n_pages][...] (up to eight)."""
         n, ptrs, sizes = self.n_pages, [], []
         for t in pools:
-            if t.size(0) != n or not t.is_contiguous() or t.get_device() != self.device.index:
+            if t.size(0) != n or not t.is_contiguous() or t.get_device() != self._index:
                 raise ValueError(f"a pool is {tuple(t.shape)} on {t.device}, not a contiguous [{n}][...] tensor on "
                                  "the device")
             ptrs.append(t.data_ptr())

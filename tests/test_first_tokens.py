@@ -176,3 +176,29 @@ def test_long_tail_behind_a_first_token(kv):
     r = want / (1.0 - want)
     assert 0.9 * n * 2.0 ** -24.8 < r < 1.1 * n * 2.0 ** -24.7
     assert float((out.double().cpu() - want).abs().max()) <= r * 2.0 ** -10, (want, float(out.min()), float(out.max()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", [1e-36, 1e-33, 1e-30, 1e30])
+def test_values_of_extreme_size(size):
+    """vq8 scales near the smallest fp32 numbers, where they are taken relative to the
+    smallest normal one, and huge ones. Outputs are within 2^-10 of the largest value:
+    the weights' parts (2^-16) and, for scales below 2^-112, half of fp32's smallest
+    step against outputs 100 times as large and more."""
+    from gqa_attention_kv_qk_gb300 import build
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    build.build()
+    lens = [300, 5, 64]
+    cfg = config(kv_dtype="vq8", batch=3, seq_len=300, window=90, first_tokens=3)
+    case = W.host_case(cfg, lens=lens)
+    case["v_values"] *= size
+    layer = DecodeLayer.for_case(case)
+    v_new = (case["v_new"].double() * size).to(torch.bfloat16).cuda()
+    q_rot = torch.empty((3, 1, 8, 128), device="cuda")
+    out = layer.step(case["q"].cuda(), case["k_new"].cuda(), v_new, q_rot=q_rot)
+    torch.cuda.synchronize()
+    assert layer.device_status() == 0
+    k, v = plain64.cached_values(layer)
+    want = plain64.attend(q_rot, k, v, lens, 90, 3)
+    err = (out.double().cpu().reshape(want.shape) - want).abs()
+    assert torch.isfinite(out).all() and float(err.max()) <= float(v.abs().max()) * 2.0 ** -10

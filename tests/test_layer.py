@@ -356,7 +356,7 @@ def test_calls_of_another_device_are_refused(monkeypatch):
     layer._outs, layer.args, layer.desc, layer.ws = {1: layer.out}, lambda *a, **k: None, None, None
     layer._reads, layer._read_args, layer._args = {1: (layer.out, layer.out)}, object(), lambda *a: None
     table = P.PageTable.__new__(P.PageTable)
-    table.device, table.args, table.ws, table.n_pages = torch.device("cuda", 1), None, None, 4
+    table._index, table.args, table.ws, table.n_pages = 1, None, None, 4
 
     class Parents:
         dtype, shape = torch.int32, table.__dict__.setdefault("seq_lens", torch.zeros(1)).shape
