@@ -328,13 +328,16 @@ def make_desc(cfg: dict) -> UaaAttnDesc:
     return d
 
 
-_raw_stream = _current_device = None
+_raw_stream = _current_device = None  # PyTorch's functions, found on first use
+_several_devices = False
 
 
 def _bind_streams():
     """PyTorch is needed here only: the rest of this module is ctypes."""
-    global _raw_stream, _current_device
+    global _raw_stream, _current_device, _several_devices
     from torch._C import _cuda_getCurrentRawStream as _raw_stream, _cuda_getDevice as _current_device
+    from torch.cuda import device_count
+    _several_devices = device_count() > 1
 
 
 def call_stream(stream, device_index: int):
@@ -342,9 +345,9 @@ def call_stream(stream, device_index: int):
     current one as a raw handle. (A torch.cuda.Stream object costs 3.5 us to make, the
     launches of a short step not much more.) The library launches on the current
     device, so another one refuses."""
-    if _current_device is None:
+    if _raw_stream is None:
         _bind_streams()
-    if _current_device() != device_index:
+    if _several_devices and _current_device() != device_index:
         raise RuntimeError(f"the tensors are on cuda:{device_index}, and the current device is "
                            f"cuda:{_current_device()}: make the call under torch.cuda.device({device_index})")
     return _raw_stream(device_index) if stream is None else stream
