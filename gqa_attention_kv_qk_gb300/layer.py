@@ -141,6 +141,10 @@ class DecodeLayer:
 
     # ------------------------------------------------------------ state
     def set_params(self, q_norm_w=None, k_norm_w=None, sink=None):
+        D, Hq = self.cfg["head_dim"], self.cfg["n_q_heads"]
+        for name, t, n in (("q_norm_w", q_norm_w, D), ("k_norm_w", k_norm_w, D), ("sink", sink, Hq)):
+            if t is not None and t.numel() != n:
+                raise ValueError(f"{name} has {t.numel()} values, the layer needs {n}")
         to = lambda t: None if t is None else t.to(device=self.device, dtype=torch.float32).contiguous()
         self.q_norm_w, self.k_norm_w, self.sink = to(q_norm_w), to(k_norm_w), to(sink)
         self._args_cache.clear()  # they hold the addresses of the ones before
@@ -226,7 +230,8 @@ class DecodeLayer:
         if T > self.max_q_len:
             raise ValueError(f"{T} tokens per sequence, the layer was built for max_q_len={self.max_q_len}")
         self.q_len = T
-        self.out_for(T, stream)
+        if T not in self._outs:
+            self.out_for(T, stream)
         return T
 
     def _bound(self, T, stream=None):
@@ -249,7 +254,13 @@ class DecodeLayer:
         return B.UaaStepArgs.from_buffer_copy(self._args(q, k_new, v_new, msl, q_rot, out))
 
     def _args(self, q, k_new, v_new, msl, q_rot, out) -> B.UaaStepArgs:
-        key = (B.ptr(q), B.ptr(k_new), B.ptr(v_new), msl, B.ptr(q_rot), B.ptr(out), self.q_len)
+        # what _build_args checks is part of the key: another tensor may come to lie there
+        key = (msl, self.q_len,
+               None if out is self._outs.get(self.q_len) else (out.data_ptr(), out.dtype, out.numel(), out.is_contiguous()),
+               None if q is None else (q.data_ptr(), q.dtype, q.numel(), q.is_contiguous(),
+                                       k_new.data_ptr(), k_new.dtype, k_new.numel(), k_new.is_contiguous(),
+                                       v_new.data_ptr(), v_new.dtype, v_new.numel(), v_new.is_contiguous()),
+               None if q_rot is None else (q_rot.data_ptr(), q_rot.dtype, q_rot.numel(), q_rot.is_contiguous()))
         a = self._args_cache.get(key)
         if a is None:
             if len(self._args_cache) > 64:
@@ -258,6 +269,18 @@ class DecodeLayer:
         return a
 
     def _build_args(self, q, k_new, v_new, max_seq_len, q_rot, out) -> B.UaaStepArgs:
+        c = self.cfg
+        io = _TORCH_DTYPE[c.get("io_dtype", "bf16")]
+        for name, t, heads, dt in (("q", q, c["n_q_heads"], io), ("k_new", k_new, c["n_kv_heads"], io),
+                                   ("v_new", v_new, c["n_kv_heads"], io),
+                                   ("q_rot", q_rot, c["n_q_heads"], torch.float32),
+                                   ("out", out, c["n_q_heads"], self.out.dtype)):
+            if t is None:
+                continue
+            n = self.batch * self.q_len * heads * c["head_dim"]
+            if t.dtype != dt or t.numel() != n or not t.is_contiguous() or t.get_device() != self._index:
+                raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}, strides {tuple(t.stride())}; a step of "
+                                 f"{self.q_len} token(s) needs {n} contiguous {dt} values on cuda:{self._index}")
         a = B.UaaStepArgs()
         a.batch = self.batch
         a.q, a.k_new, a.v_new = B.ptr(q), B.ptr(k_new), B.ptr(v_new)
@@ -284,7 +307,7 @@ class DecodeLayer:
         capacity would end by it)."""
         s = B.call_stream(stream, self._index)
         T = self._begin(q, stream)
-        want = self.out_for(T)
+        want = self._outs[T]
         if out is not None:
             assert out.shape == want.shape and out.dtype == want.dtype and out.is_contiguous()
         msl = self._bound(T, stream) if max_seq_len is None else int(max_seq_len)

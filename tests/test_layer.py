@@ -348,6 +348,7 @@ def test_calls_of_another_device_are_refused(monkeypatch):
         if name.startswith("uaa_"):
             monkeypatch.setattr(binding, name, launched)
     monkeypatch.setattr(binding, "_current_device", lambda: 0)
+    monkeypatch.setattr(binding, "_several_devices", True)
     monkeypatch.setattr(binding, "_raw_stream", lambda index: 0)
     layer = L.DecodeLayer.__new__(L.DecodeLayer)
     layer.cfg, layer.batch, layer.max_q_len, layer._index, layer.device = config(), 1, 4, 1, torch.device("cuda", 1)
@@ -375,3 +376,40 @@ def test_calls_of_another_device_are_refused(monkeypatch):
                 call()
     layer._index = 0
     assert binding.call_stream(None, 0) == 0 and binding.call_stream(0x77, 0) == 0x77
+
+
+# ---------------------------------------------------------------- tensors of a step
+
+def test_tensors_that_do_not_fit_are_refused(monkeypatch):
+    """A step's tensors reach the library as addresses: another type, size, device or
+    stride would be read past or as something else."""
+    from gqa_attention_kv_qk_gb300 import layer as L
+    layer = L.DecodeLayer.__new__(L.DecodeLayer)
+    layer.cfg, layer.batch, layer._index, layer.device = config(), 3, -1, torch.device("cpu")
+    layer.q_len, layer.page_size, layer.capacity, layer._args_cache = 2, 0, 64, {}
+    layer.out, layer._outs = torch.zeros(3, 4, 64), {}
+    layer.q_norm_w = layer.k_norm_w = layer.sink = layer.k_scale = layer.v_scale = None
+    layer.k_cache = layer.v_cache = layer.seq_lens = torch.zeros(4)
+    bf, f4 = torch.bfloat16, torch.float32
+    ok = dict(q=torch.zeros(3, 2, 4, 64, dtype=bf), k_new=torch.zeros(3, 2, 2, 64, dtype=bf),
+              v_new=torch.zeros(3, 2, 2, 64, dtype=bf), q_rot=torch.zeros(3, 2, 4, 64), out=torch.zeros(3, 2, 4, 64))
+
+    def build(**kw):
+        x = {**ok, **kw}
+        return layer._args(x["q"], x["k_new"], x["v_new"], 5, x["q_rot"], x["out"])
+
+    assert build().q == ok["q"].data_ptr() and build(q_rot=None).q_rot in (None, 0)
+    qkv = torch.zeros(3, 2, 8 * 64, dtype=bf)                        # a fused projection's output
+    for name, bad in (("q", qkv[..., :256].unflatten(-1, (4, 64))), ("k_new", qkv[..., 256:384]), ("q", ok["q"].to(f4)),
+                      ("q", ok["q"][:, :1]), ("v_new", ok["q"]), ("k_new", ok["k_new"].to(torch.float16)),
+                      ("q_rot", ok["q_rot"].to(bf)), ("out", ok["out"].to(bf)), ("out", ok["out"][:2])):
+        with pytest.raises(ValueError, match=f"^{name} is"):
+            build(**{name: bad})
+    layer._index = 0                                                 # of the device: these are the host's
+    layer._args_cache.clear()
+    with pytest.raises(ValueError, match="^q is .* on cuda:0"):
+        build()
+    for name, n in (("q_norm_w", 64), ("k_norm_w", 64), ("sink", 4)):
+        layer.set_params(**{name: torch.ones(n)})
+        with pytest.raises(ValueError, match=f"{name} has {n + 1} values, the layer needs {n}"):
+            layer.set_params(**{name: torch.ones(n + 1)})
