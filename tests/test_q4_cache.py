@@ -565,3 +565,58 @@ def test_batches_of_more_than_one_slice(T, page, D):
     want = plain64.attend(q_rot[some], k[some], v[some], [lens[b] for b in some], 20, 3)
     err = (out.double().cpu().reshape(n, T, 2, D)[some] - want).abs()
     assert float(err.max()) <= TOL_MAX and float(err.mean()) <= TOL_MEAN
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D,page", [(1, 256, 0), (3, 256, 0), (40, 128, 0), (1, 256, 64), (64, 128, 64)])
+def test_rows_past_4_gib(T, D, page):
+    """Sequences whose codes lie past 2^32 bytes of the cache (or on such pages of a pool)
+    give what they give in a small cache; so does the reader, and a copy of such pages."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    Bn, Hkv, cap = 3, 8, 1024
+    cfg = config(n_q_heads=32, n_kv_heads=Hkv, head_dim=D, batch=Bn, seq_len=500, q_len=T, page_size=page,
+                 reproducible=True)
+    lens = [500, 0, 77]
+    case = W.host_case(cfg, lens=lens, cap=cap)
+    small = DecodeLayer.for_case(case)
+    rows = 2 ** 32 // (D // 2) + 10 * Hkv * cap        # past 2^32 bytes of codes
+    if page:
+        n = rows // (Hkv * page)
+        table = torch.arange(n - Bn * cap // page, n, dtype=torch.int32).flip(0).reshape(Bn, -1)
+        big = DecodeLayer(cfg, Bn, cap, page_size=page, block_table=table, n_pages=n, max_q_len=T)
+        at = lambda x: x
+    else:
+        n = rows // (Hkv * cap)
+        big = DecodeLayer(dict(cfg, batch=n), n, cap, max_q_len=T)
+        at = lambda x: x[n - Bn:]
+        big.seq_lens.fill_(-1)
+    at(big.seq_lens).copy_(small.seq_lens)
+    big.max_len_hint = small.max_len_hint
+    for name in ("k_cache", "v_cache", "k_scale", "v_scale"):
+        x = small.logical(name)
+        if page:
+            big._to_pool(x, getattr(big, name))
+        else:
+            at(getattr(big, name)).copy_(x)
+    assert big.k_cache.numel() > 2 ** 32
+    dev = {k: case[k].cuda() for k in ("q", "k_new", "v_new")}
+    want = small.step(*dev.values())
+    if not page:                                        # the other sequences are idle
+        dev = {k: torch.cat((torch.zeros((n - Bn, *x.shape[1:]), dtype=x.dtype, device="cuda"), x)) for k, x in dev.items()}
+    got = big.step(*dev.values())
+    torch.cuda.synchronize()
+    assert small.device_status() == 0 and big.device_status() == 0
+    assert float((at(got) - want).abs().max()) <= TOL_MAX  # ranges are cut elsewhere
+    for name in ("k_cache", "v_cache", "k_scale", "v_scale"):
+        assert torch.equal(at(big.logical(name)), small.logical(name))
+    for a, b in zip(small.read_rows(None, 600), big.read_rows(None, 600)):
+        assert torch.equal(at(b), a)
+    if page:
+        from gqa_attention_kv_qk_gb300.pages import PageTable
+        pages = PageTable(big.block_table, page, n, seq_lens=big.seq_lens)
+        assert pages.block_table is big.block_table
+        pages.compact()
+        pages.copy_layer(big)
+        assert pages.block_table.max() < Bn * cap // page and pages.device_status() == 0
+        for a, b in zip(small.read_rows(None, 600), big.read_rows(None, 600)):
+            assert torch.equal(b, a)
