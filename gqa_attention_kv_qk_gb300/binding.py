@@ -284,7 +284,7 @@ def uaa_abi_version() -> int:
     return int(lib().uaa_abi_version())
 
 
-UAA_STATIC_SCRATCH_BYTES = 8 << 20
+UAA_STATIC_SCRATCH_BYTES = (8 << 20) + (16 << 10)
 
 
 def uaa_decode_attn_static(desc, args, stream=None, check=True) -> int:

@@ -469,7 +469,7 @@ const char* uaa_status_string(uaa_status status);
 int32_t uaa_abi_version(void);
 
 /* Bytes of the library's built-in scratch array (see uaa_decode_attn_static). */
-#define UAA_STATIC_SCRATCH_BYTES (8u << 20)
+#define UAA_STATIC_SCRATCH_BYTES ((8u << 20) + (16u << 10))
 
 /* uaa_decode_attn without a caller workspace. The pages have no counterpart of
  * this entry point: it exists for callers that cannot allocate device memory
@@ -478,7 +478,8 @@ int32_t uaa_abi_version(void);
  * must never block on the allocator's implicit device synchronisation.
  *
  * The split partials, rotated q rows and status word then live in one
- * file-scope __device__ array of UAA_STATIC_SCRATCH_BYTES (8 MiB) that every
+ * file-scope __device__ array of UAA_STATIC_SCRATCH_BYTES (8 MiB, and 16 KiB for the
+ * parts that keep their places) that every
  * GPU which loads the library holds until the process exits. The caller still
  * passes every input and output in args; this call allocates nothing (no
  * cudaMalloc, cudaFree or allocating library routine).

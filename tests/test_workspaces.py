@@ -163,3 +163,22 @@ def test_layers_that_share_a_workspace():
     with pytest.raises(B.UaaError, match="16-byte aligned"):
         layer = DecodeLayer(cfgs[5], batch, cap, workspace=shared[8:])
         layer.step(*rows(cfgs[5], batch, 1, 0))
+
+
+def test_fixed_parts_take_nothing_from_the_built_in_scratch():
+    """Every step whose arrays fitted 8 MiB beside a range balance of its own size fits
+    the built-in scratch, whose fixed parts are sized for the largest grid."""
+    al = lambda x: (x + 255) // 256 * 256
+    tight = 0
+    for kv, D, heads, kv_heads in (("bf16", 128, 32, 8), ("q4", 64, 64, 8), ("vq8", 64, 64, 8), ("f32", 64, 32, 8),
+                                   ("q8", 256, 16, 8)):
+        d = B.make_desc(config(kv_dtype=kv, head_dim=D, n_q_heads=heads, n_kv_heads=kv_heads))
+        for n_sm in (148, 152):
+            for batch in range(1, 700):
+                lay = B.uaa_get_workspace_layout(d, batch, 4000, n_sm, 1)
+                P = lay.n_ctas
+                own = 256 + 256 + al(8 * P) + 2 * al(4 * P) + al(4 * (P + 1)) + lay.total_bytes - lay.q_rot_offset
+                if own <= 8 << 20:
+                    assert lay.total_bytes <= B.UAA_STATIC_SCRATCH_BYTES
+                    tight += lay.total_bytes > 8 << 20
+    assert tight > 0
