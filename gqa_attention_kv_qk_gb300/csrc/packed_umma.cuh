@@ -14,8 +14,8 @@
 // Step s of an item (tile s % 2):
 //   S (128 x 128, fp32) = Q . K^T, Q rows in shared memory (K-major, 128-byte swizzle);
 //   softmax: the running maximum m is raised only where a logit exceeds it by more than
-//     2^8 (the final division cancels m); P = exp2(S - m) over S's columns as bf16, and the
-//     row's sum of the weights before they are rounded;
+//     2^8 (the final division cancels m); P = exp2(S - m) over S's columns as two bf16 parts,
+//     and the row's sum of the weights before they are split;
 //   O (128 x D, fp32) += P . V, P from tensor memory.
 // The MMA lane issues S of step s + 2 right after P . V of step s (they share columns and
 // run in order), while the other tile's softmax runs; an item's first S beside the epilogue of
@@ -26,17 +26,19 @@
 // stages; the warps that bring q' widen them into the ring's tiles.
 //
 // Rounding: q' enters as bf16 hi + lo parts (2^-16 relative), two MMAs each, so that logits
-// of any size keep their last bits. The weights enter as bf16, rounded to nearest (at most
-// 2^-9 relative, the bf16 output's own rounding), or, for fp32 outputs, as hi + lo parts by
-// truncation (2^-14).
+// of any size keep their last bits. The weights (8-bit caches: times the value's scale) enter as
+// bf16 hi + lo parts too (hi truncated, the rest rounded to nearest: 2^-15 relative), two MMAs
+// each, as in the steps of equal lengths. One part, 2^-8 at most, would be the largest error of a
+// bf16 output beside its own rounding (0.0020 to 0.0024 relative to 64 bits against 0.0017), for 843
+// instead of 1,002 us for the two chunks below.
 //
 // What bounds it. Decodes: the cache's bytes (64 requests of up to 16,000 tokens, head_dim
-// 128: 332 us, 6.4 TB/s). Long prompts: the chain of a tile's step, softmax -> P . V -> S (8,191
-// tokens at once 560 us, 982 TFLOP/s; two chunks of 1,000 behind 20,000 to 32,000 cached 842
-// us; the tensor pipe is some 60 % busy, q' in two parts counted). In that chain instruction
-// fetch weighs most: with the weights in a loop of 32 columns and mask and softcap in one of 16,
+// 128: 343 us, 6.2 TB/s). Long prompts: the chain of a tile's step, softmax -> P . V -> S (8,191
+// tokens at once 660 us, 833 TFLOP/s; two chunks of 1,000 behind 20,000 to 32,000 cached 1,002
+// us; q' and P in two parts make twice those operations in MMAs). In that chain instruction
+// fetch weighed most: with the weights in a loop of 32 columns and mask and softcap in one of 16,
 // against all 128 unrolled, chunks went from 881 to 842 us, a mixed batch from 332 to 304 and
-// 8-bit drafts from 115 to 87. Short items: their own latency.
+// 8-bit drafts from 115 to 87 (the weights in one part then). Short items: their own latency.
 //
 // Warps (512 threads): 0 and 3 TMA (keys and values, through one ring in the order of their
 // first use), 1 MMA issue and TMEM, 2 takes items from the
@@ -222,14 +224,14 @@ __device__ __forceinline__ void issue_qk(uint32_t lead, uint32_t t_s, uint64_t q
     }
 }
 
-// Half of O += P . V: keys 16 FROM .. + 63, the parts of P on each chunk of V.
-template <int FROM, int PARTS>
+// Half of O += P . V: keys 16 FROM .. + 63, both parts of P on each chunk of V.
+template <int FROM>
 __device__ __forceinline__ void issue_pv(uint32_t lead, uint32_t t_o, uint32_t t_p, uint64_t vd, uint32_t idesc, uint32_t more)
 {
 #pragma unroll
     for (int k2 = FROM; k2 < FROM + 4; ++k2)
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part)
+        for (int part = 0; part < 2; ++part)
             ptx::umma_bf16_ts_lead(lead, t_o, t_p + p_col(k2, part), vd + ((k2 * 2048) >> 4), idesc,
                                    (part > 0 || k2 > FROM) ? 1u : more);
 }
@@ -344,7 +346,7 @@ __device__ __noinline__ void merge_pieces(const PackedUmmaParams& p, const PkIte
     else merge_rows<D, F32, 4, 4>(p, it, rr0, n, n_pieces, quad, lane);
 }
 
-// F32: fp32 outputs, P in two parts
+// F32: fp32 outputs
 template <int D, int KV, bool F32>
 __global__ void __launch_bounds__(kPkThreads, 1)
 packed_umma_kernel(const __grid_constant__ PackedMaps tm, const PackedUmmaParams p)
@@ -689,9 +691,9 @@ packed_umma_kernel(const __grid_constant__ PackedMaps tm, const PackedUmmaParams
                         if (fresh && !v_here) ok = ok && ptx::mbar_wait(bar_full + 8 * vs, v_par, kWaitLimitCycles);
                         __syncwarp();
                         ptx::tc_fence_after();
-                        issue_pv<0, F32 ? 2 : 1>(lead, tmem + 256 + 128 * x, tmem + 128 * x, vd, kIdO, s >= 4);  // (4: O has a step's sum)
+                        issue_pv<0>(lead, tmem + 256 + 128 * x, tmem + 128 * x, vd, kIdO, s >= 4);  // (4: O has a step's sum)
                         look_for_k();
-                        issue_pv<4, F32 ? 2 : 1>(lead, tmem + 256 + 128 * x, tmem + 128 * x, vd, kIdO, 1u);
+                        issue_pv<4>(lead, tmem + 256 + 128 * x, tmem + 128 * x, vd, kIdO, 1u);
                         if (done) free_tile(vs);
                         if (s >= n_steps) ptx::umma_commit_lead(lead, bar_o + 8 * x);
                         if (s == n_steps + 1) ptx::umma_commit_lead(lead, bar_idone);
@@ -971,19 +973,15 @@ packed_umma_kernel(const __grid_constant__ PackedMaps tm, const PackedUmmaParams
                                 e0 *= k & 1 ? vs4.z : vs4.x;
                                 e1 *= k & 1 ? vs4.w : vs4.y;
                             }
-                            if (F32) {
-                                const uint32_t b0 = __float_as_uint(e0) & 0xffff0000u, b1 = __float_as_uint(e1) & 0xffff0000u;
-                                hh[k] = __byte_perm(b0, b1, 0x7632);
-                                const float2 rest = ptx::add_f32x2(make_float2(e0, e1), make_float2(-__uint_as_float(b0), -__uint_as_float(b1)));
-                                lo16[k] = __byte_perm(__float_as_uint(rest.x), __float_as_uint(rest.y), 0x7632);
-                            } else {
-                                hh[k] = pk_pack(e0, e1);
-                            }
+                            const uint32_t b0 = __float_as_uint(e0) & 0xffff0000u, b1 = __float_as_uint(e1) & 0xffff0000u;
+                            hh[k] = __byte_perm(b0, b1, 0x7632);
+                            const float2 rest = ptx::add_f32x2(make_float2(e0, e1), make_float2(-__uint_as_float(b0), -__uint_as_float(b1)));
+                            lo16[k] = pk_pack(rest.x, rest.y);
                             if (k & 1) s1 = ptx::add_f32x2(s1, e);
                             else s0 = ptx::add_f32x2(s0, e);
                         }
                         ptx::tmem_st16(t_s + h, hh);
-                        if (F32) ptx::tmem_st16(t_s + h + 16, lo16);
+                        ptx::tmem_st16(t_s + h + 16, lo16);
                     }
                     l += (s0.x + s0.y) + (s1.x + s1.y);
                     ptx::tmem_wait_st();

@@ -534,8 +534,8 @@ uaa_status uaa_packed_append(const uaa_attn_desc* desc, const uaa_packed_args* a
  * one append more than once. bf16, vq8 and q8 caches at head_dim 64 and 128 are attended by
  * the tcgen05 kernel, 4-bit ones, head_dim 256, and 8-bit ones where q_len says that a
  * request has no more than 16 query rows per kv head by the split-K kernel, fp32 ones
- * in fp32. With a bf16 output the attention weights enter the tcgen05 kernel as one bf16 part
- * (2^-9 relative each), with an fp32 output as two (2^-14). */
+ * in fp32. The attention weights enter the tcgen05 kernel as two bf16 parts (2^-15 relative)
+ * whatever the output's type. */
 uaa_status uaa_packed_attn(const uaa_attn_desc* desc, const uaa_packed_args* args, const uaa_workspace* ws,
                            cudaStream_t stream);
 
