@@ -396,7 +396,8 @@ class DecodeLayer:
                 continue
             strided = name in ("q", "k_new", "v_new")  # rows of a joint projection
             good = (t.dtype == dt and tuple(t.shape) == (N, heads, D) and t.get_device() == self._index
-                    and (t.is_contiguous() or (strided and t.stride(2) == 1 and (heads == 1 or t.stride(1) == D))))
+                    and (t.is_contiguous() or (strided and t.stride(2) == 1 and (heads == 1 or t.stride(1) == D)
+                                               and t.stride(0) >= heads * D)))
             if not good:
                 raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}, strides {tuple(t.stride())}; a packed step "
                                  f"needs {(N, heads, D)} {dt} on cuda:{self._index}" + (", its heads dense" if strided else ", dense"))

@@ -18,3 +18,22 @@ def _built():
 
 def rows(n, heads, seed=0):
     return torch.randn((n, heads, 64), generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16).cuda()
+
+
+@pytest.mark.parametrize("which", ["q", "k", "v"])
+def test_tokens_that_share_one_row_are_refused(which):
+    """expand() gives a stride of 0 between tokens, which the C entries take as dense rows."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    from gqa_attention_kv_qk_gb300.packed import PackedPlan
+    layer, plan = DecodeLayer(CFG, 2, 128, max_tokens=8), PackedPlan(2, 8)
+    x = dict(q=rows(8, 8), k=rows(8, 2), v=rows(8, 2))
+    x[which] = x[which][:1].expand(8, -1, -1)
+    with pytest.raises(ValueError, match="strides"):
+        layer.step_packed(x["q"], x["k"], x["v"], plan)
+    with pytest.raises(ValueError, match="strides"):
+        layer.append_packed(x["q"], x["k"], x["v"], plan)
+    # one token has no neighbour: its stride says nothing
+    one = PackedPlan(2, 1)
+    layer.plan(torch.tensor([1, 0], dtype=torch.int32, device="cuda"), one)
+    layer.step_packed(rows(1, 8).expand(1, -1, -1), rows(1, 2), rows(1, 2), one)
+    assert layer.seq_lens.tolist() == [1, 0]
