@@ -280,7 +280,8 @@ __device__ void build_schedule(const ScheduleParams& s, int* sm)
     }
 
     // the entries, with the places in the records and the counters of what is cut (a pair
-    // whose records or counters would not fit stays whole)
+    // whose records, counters or entries would not fit stays whole; each pair after it keeps
+    // room for one entry, max_entries being max_pairs at least)
     int n_entries = 0, n_rec = 0, n_groups = 0, before = 0;  // (before: cost of the beyond-pairs so far)
     for (int r0 = 0; r0 < n_pairs; r0 += nthr) {
         const int r = r0 + tid;
@@ -301,8 +302,12 @@ __device__ void build_schedule(const ScheduleParams& s, int* sm)
         const int rec = n_rec + cta_prefix(static_cast<int>(min(want, static_cast<long long>(s.max_rec_rows) + 1)), buf, n_take);
         const int group = n_groups + cta_prefix(n > 1 ? 1 : 0, buf, n_cut);
         if (rec + want > s.max_rec_rows || (group + 1) * 2 * s.Hkv > s.max_counters) n = min(n, 1);
-        const int at = n_entries + cta_prefix(n, buf, n_all);
-        for (int k = 0; k < n && at + k < s.max_entries; ++k)
+        int at = n_entries + cta_prefix(n, buf, n_all);
+        if (n_entries + n_all > s.max_entries - max(0, n_pairs - r0 - nthr)) {  // (the same for all threads)
+            if (at + n > s.max_entries - (n_pairs - 1 - r)) n = min(n, 1);
+            at = n_entries + cta_prefix(n, buf, n_all);
+        }
+        for (int k = 0; k < n; ++k)
             s.entries[at + k] = PackedEntry{p.b, p.rp, k | n << 16, group, p.row0, p.T, p.end, rec};
         if (n > 1)
             for (int h = 0; h < 2 * s.Hkv; ++h) s.counters[group * 2 * s.Hkv + h] = 0u;
@@ -313,7 +318,7 @@ __device__ void build_schedule(const ScheduleParams& s, int* sm)
     if (tid == 0) {
         s.header[0] = static_cast<unsigned>(s.n_sm);                  // the next item after each CTA's first
         s.header[2] = 0u;                                             // CTAs that came to the list's end
-        s.header[1] = static_cast<unsigned>(min(n_entries, s.max_entries));  // entries
+        s.header[1] = static_cast<unsigned>(n_entries);               // entries
     }
 }
 
