@@ -97,13 +97,15 @@ __device__ __forceinline__ float2 sum_two(float a, float b)
     return make_float2(sum, __fadd_rn(__fsub_rn(a, __fsub_rn(sum, bb)), __fsub_rn(b, bb)));
 }
 
-// a c - b s as the nearest float (nearly always), every operand a sum of two (x: the float, y: what it lacks).
+// a c - b s as the nearest float (nearly always), every operand a sum of two (x: the float, y: what it
+// lacks). A sum that is infinite, of infinite operands or past the largest float, stays so: what it
+// lacks is no number then.
 __device__ __forceinline__ float dot_two(float2 a, float2 b, float2 c, float2 s)
 {
     const float p = __fmul_rn(a.x, c.x), q = -__fmul_rn(b.x, s.x);
     const float2 sum = sum_two(p, q);
     const float rest = (fmaf(a.x, c.x, -p) - fmaf(b.x, s.x, q)) + fmaf(a.x, c.y, -b.x * s.y) + fmaf(a.y, c.x, -b.y * s.x);
-    return sum.x + (sum.y + rest);
+    return isinf(sum.x) ? sum.x : sum.x + (sum.y + rest);
 }
 
 // Q4: a 4-bit cache. NORM: q and k rows are normed. Template arguments, as they cost the

@@ -60,3 +60,58 @@ def test_bf16_outputs_are_rounded_once(kv, D, G):
     slack = slack_before_rounding(cfg, s, q_rot)
     err = (out - want).abs()
     assert bool((err <= half_step(want.abs() + slack) + slack).all()), float((err > half_step(want.abs() + slack) + slack).double().mean())
+
+
+@pytest.mark.parametrize("style", ["neox", "interleaved"])
+def test_bf16_keys_with_a_norm_are_rounded_once(style):
+    """A million appended elements: each the exact key rounded to bf16, but for the fp32 value's own
+    error. cos and sin are sums of two floats within 2^-26, so the pair (a, b) is off by at most
+    2^-26 (|a| + |b|) <= 2^-25 of its length; norm, products and sums of two floats are off by far less;
+    and the value is rounded to fp32 first, 2^-24. (Norm and rotation in plain fp32 are off by some
+    2^-22 of the length, and dozens of these elements land outside.)"""
+    cfg = dict(n_q_heads=8, n_kv_heads=8, head_dim=128, kv_dtype="bf16", io_dtype="bf16", out_dtype="f32", rope_theta=10000.0,
+               rope_style=style, qk_norm=True)
+    s = make_step(cfg, [(0, 600), (400, 400)], 1024, page=32, seed=11)
+    plan = make_plan(s)
+    s["layer"].append_packed(s["q"], s["k"], s["v"], plan)
+    k = s["layer"].read_packed(plan)[0].double().cpu()
+    from tests.test_packed import pair_positions, turned
+    r = 0
+    for n, T in zip(s["lens"], s["new"]):
+        exact = turned(cfg, s["k"][r:r + T], s["layer"].k_norm_w, pair_positions(cfg, s, r, n, T))
+        if style == "neox":
+            a, b = exact.chunk(2, -1)
+            length = torch.sqrt(a * a + b * b).repeat(1, 1, 2)
+        else:
+            a, b = exact[..., ::2], exact[..., 1::2]
+            length = torch.sqrt(a * a + b * b).repeat_interleave(2, -1)
+        own = 2.0 ** -24 * 1.01 * exact.abs() + 2.0 ** -25 * length
+        assert bool(((k[r:r + T] - exact).abs() <= half_step(exact.abs() + own) + own).all())
+        r += T
+
+
+@pytest.mark.parametrize("kv", ["bf16", "vq8"])
+@pytest.mark.parametrize("style", ["neox", "interleaved"])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_infinite_keys_stay_infinite(kv, style, io):
+    """An infinite element turns into infinities of the formula's signs, a sum beyond the largest
+    number into an infinity, a NaN stays one; other pairs are as they were."""
+    cfg = dict(n_q_heads=4, n_kv_heads=2, head_dim=64, kv_dtype=kv, io_dtype=io, out_dtype="f32", rope_theta=10000.0, rope_style=style)
+    s = make_step(cfg, [(1, 40), (100, 1), (30, 2)], 128, page=32, seed=6)
+    k = s["k"]
+    inf, big = float("inf"), 3.3e38
+    k[3, 0, 5], k[3, 1, 40], k[17, 0, 0], k[40, 1, 63], k[41, 0, 9], k[42, 1, 10] = inf, -inf, -inf, inf, float("nan"), inf
+    k[20, 0, [0, 1, 32, 33]] = big  # (pairs of either style: their sums pass the largest bf16)
+    plan = make_plan(s)
+    s["layer"].append_packed(s["q"], k, s["v"], plan)
+    got = s["layer"].read_packed(plan)[0].double().cpu()
+    from tests.test_packed import pair_positions, turned
+    exact = torch.cat([turned(cfg, k[r:r + T], None, pair_positions(cfg, s, r, n, T)) for r, n, T in ((0, 1, 40), (40, 100, 1), (41, 30, 2))])
+    # (numbers beyond the largest bf16, 2^128 - 2^120, and half a step more are infinities)
+    exact = torch.where(exact.abs() >= 2.0 ** 128 - 2.0 ** 119, exact.sign() * inf, exact)
+    assert int(torch.isinf(exact).sum()) >= 11 and int(torch.isnan(exact).sum()) == 2
+    assert torch.equal(torch.isnan(got), torch.isnan(exact))
+    assert torch.equal(torch.isinf(got), torch.isinf(exact)) and bool((got[torch.isinf(exact)] == exact[torch.isinf(exact)]).all())
+    fine = torch.isfinite(exact)
+    # 2^-8 relative and the rounding to fp32 of terms up to the pair's length, here 6 or big
+    assert bool(((got - exact).abs()[fine] <= half_step(exact)[fine] + 2.0 ** -22 * torch.where(exact.abs() > 1e30, big, 6.0)[fine]).all())
