@@ -7,6 +7,7 @@ makes: build the layer, load or grow its cache, then `step(q, k_new, v_new)`.
 from __future__ import annotations
 
 import contextlib
+import weakref
 
 import torch
 
@@ -37,6 +38,19 @@ def _memory_of(stream, index):
     return torch.cuda.stream(stream)
 
 
+class _Workspace:
+    """What the layers that share a workspace tensor know of it: appended, the layer, the plan
+    and the plan's count of fillings whose q rows and work list lie there."""
+
+    __slots__ = ("appended", "__weakref__")
+
+    def __init__(self):
+        self.appended = None
+
+
+_workspaces = weakref.WeakValueDictionary()  # by device and address, as long as a layer holds the tensor
+
+
 class DecodeLayer:
     """page_size: store the caches as pools of pages of that many positions;
     block_table ([batch][capacity / page_size] int32, default: sequence b takes
@@ -52,8 +66,6 @@ class DecodeLayer:
     the most rows a packed step takes (step_packed; 0: none).
     cfg's rope_sections and rope_axes: rotary positions of several axes in packed steps
     (packed.pair_axes), rotation pairs per axis and their order, "blocks" or "cycle"."""
-
-    _appended = None  # the plan whose q rows and work list are in the workspace
 
     def __init__(self, cfg: dict, batch: int, capacity: int, device="cuda", page_size=None, block_table=None,
                  n_pages=None, max_q_len=1, cache=None, workspace=None, max_tokens=0):
@@ -133,6 +145,7 @@ class DecodeLayer:
                              f"contiguous bytes (uint8) on its device")
         self.ws_tensor = w
         self.ws = B.UaaWorkspace(w.data_ptr(), w.numel())
+        self._shared = _workspaces.setdefault((self._index, w.data_ptr()), _Workspace())
 
     @classmethod
     def for_case(cls, case: dict, device="cuda") -> "DecodeLayer":
@@ -369,6 +382,17 @@ class DecodeLayer:
         B.uaa_contiguous_plan(plan.with_lens(q_lens, self.batch, self._index), B.ptr(self.seq_lens), self.capacity, self.ws, s)
         return plan
 
+    @property
+    def _appended(self):
+        """The plan whose q rows and work list are in the workspace: this layer's last append
+        there, and the plan not filled anew since (else None)."""
+        a = self._shared.appended
+        return a[1] if a is not None and a[0]() is self and a[2] == a[1].filled else None
+
+    @_appended.setter
+    def _appended(self, plan):
+        self._shared.appended = None if plan is None else (weakref.ref(self), plan, plan.filled)
+
     def _packed_args(self, q, k_new, v_new, plan, positions, out, q_rot, max_q_len) -> B.UaaPackedArgs:
         """The packed step's arguments (built once per distinct set of tensors, as _args)."""
         ts = (q, k_new, v_new, out, q_rot, positions)
@@ -444,7 +468,8 @@ class DecodeLayer:
                 if len(self._packed_out) < 16:  # kept for good: a captured graph may write them
                     self._packed_out[plan.n_tokens] = out
         B.uaa_packed_step(self.desc, self._packed_args(q, k_new, v_new, plan, positions, out, None, max_q_len), self.ws, s)
-        self._packed_lengths(plan)
+        self._packed_lengths()
+        self._appended = plan
         return out
 
     def append_packed(self, q, k_new, v_new, plan, positions=None, q_rot=None, stream=None):
@@ -453,21 +478,24 @@ class DecodeLayer:
         workspace, for attend_packed."""
         s = B.call_stream(stream, self._index)
         B.uaa_packed_append(self.desc, self._packed_args(q, k_new, v_new, plan, positions, None, q_rot, None), self.ws, s)
-        self._packed_lengths(plan if q_rot is None else self._appended)
+        self._packed_lengths()
+        if q_rot is None:
+            self._appended = plan
 
     def attend_packed(self, plan, out, max_q_len=None, stream=None):
-        """The attention alone, after append_packed by the same plan (any number of times)."""
+        """The attention alone, after append_packed by the same plan (any number of times): the
+        last step on the layer's workspace, and the plan as it was filled for it."""
         if self._appended is not plan:
-            raise ValueError("attend_packed follows append_packed (without q_rot) or step_packed by the same plan")
+            raise ValueError("attend_packed follows append_packed (without q_rot) or step_packed by the same plan, with no "
+                             "other step on the layer's workspace and no other filling of the plan between")
         s = B.call_stream(stream, self._index)
         B.uaa_packed_attn(self.desc, self._packed_args(None, None, None, plan, None, out, None, max_q_len), self.ws, s)
         return out
 
-    def _packed_lengths(self, plan):
+    def _packed_lengths(self):
         """A packed step takes each request as far as the plan says, up to the capacity: the
         bound that the next step of equal lengths goes by is read when it comes."""
         self.max_len_hint = self.capacity
-        self._appended = plan
 
     def read_packed(self, plan, stream=None):
         """The cached keys and values of a plan's rows, [n_tokens][Hkv][D] in the layer's out
@@ -499,6 +527,7 @@ class DecodeLayer:
 
     def partial(self, stream=None):
         s = B.call_stream(stream, self._index)
+        self._appended = None
         B.uaa_decode_attn_partial(self.desc, self.args(None, None, None), self.ws, s)
 
     def combine(self, stream=None):

@@ -33,6 +33,7 @@ class PackedPlan:
         self.device = dev = dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
         self._index = dev.index
         self.batch, self.n_tokens = int(batch), int(n_tokens)
+        self.filled = 0  # how often plan() has filled it
         new = lambda n, dt=torch.int32: torch.full((n,), -1, dtype=dt, device=dev)
         self.q_starts = torch.zeros(self.batch + 1, dtype=torch.int32, device=dev)
         self.kv_ends = new(self.batch)
@@ -43,13 +44,15 @@ class PackedPlan:
         a.token_seq, a.positions, a.slots = B.ptr(self.token_seq), B.ptr(self.positions), B.ptr(self.slots)
 
     def with_lens(self, q_lens, batch: int, index: int):
-        """The plan's arguments for the requests' token counts (int32 [batch] on the device)."""
+        """The plan's arguments for the requests' token counts (int32 [batch] on the device), to be
+        filled by them."""
         if self.batch != batch or self._index != index:
             raise ValueError(f"the plan is for {self.batch} requests on cuda:{self._index}, not {batch} on cuda:{index}")
         if (q_lens.dtype is not torch.int32 or q_lens.shape != self.kv_ends.shape or q_lens.get_device() != index
                 or not q_lens.is_contiguous()):
             raise ValueError("q_lens is not a contiguous int32 tensor [batch] on the device")
         self.args.q_lens = q_lens.data_ptr()
+        self.filled += 1
         return self.args
 
 

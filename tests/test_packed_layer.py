@@ -37,3 +37,43 @@ def test_tokens_that_share_one_row_are_refused(which):
     layer.plan(torch.tensor([1, 0], dtype=torch.int32, device="cuda"), one)
     layer.step_packed(rows(1, 8).expand(1, -1, -1), rows(1, 2), rows(1, 2), one)
     assert layer.seq_lens.tolist() == [1, 0]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "q4", "f32"])
+def test_attention_after_another_append(kv):
+    """attend_packed needs the layer's own append by the plan as it stands, the last one on its workspace."""
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    from gqa_attention_kv_qk_gb300.packed import PackedPlan
+    cfg = dict(CFG, kv_dtype=kv)
+    a = DecodeLayer(cfg, 2, 128, max_tokens=8)
+    b = DecodeLayer(cfg, 2, 128, max_tokens=8, workspace=a.ws_tensor)
+    view = DecodeLayer(cfg, 2, 128, max_tokens=8, workspace=a.ws_tensor[:])
+    plan, out = PackedPlan(2, 8), torch.zeros((8, 8, 64), device="cuda")
+    x = rows(8, 8), rows(8, 2, 1), rows(8, 2, 2)
+    q_lens = torch.tensor([3, 5], dtype=torch.int32, device="cuda")
+    a.plan(q_lens, plan)
+    a.append_packed(*x, plan)
+    assert a.attend_packed(plan, out) is out
+    for other in (b, view):
+        a.append_packed(*x, plan)
+        other.append_packed(*x, plan)
+        with pytest.raises(ValueError, match="append_packed"):
+            a.attend_packed(plan, out)
+        other.attend_packed(plan, out)
+    a.append_packed(*x, plan)
+    b.step(torch.zeros((2, 8, 64), dtype=torch.bfloat16, device="cuda"), rows(2, 2), rows(2, 2))
+    with pytest.raises(ValueError, match="append_packed"):
+        a.attend_packed(plan, out)
+    a.step_packed(*x, plan)
+    a.attend_packed(plan, out)
+    a.plan(q_lens, plan)  # refilled, for other lengths by now
+    with pytest.raises(ValueError, match="append_packed"):
+        a.attend_packed(plan, out)
+    a.append_packed(*x, plan)
+    assert a.attend_packed(plan, out) is out and a.device_status() == 0
+    # a workspace of its own is not concerned
+    alone = DecodeLayer(cfg, 2, 128, max_tokens=8)
+    alone.plan(q_lens, plan)
+    alone.append_packed(*x, plan)
+    b.step(torch.zeros((2, 8, 64), dtype=torch.bfloat16, device="cuda"), rows(2, 2), rows(2, 2))
+    alone.attend_packed(plan, out)
