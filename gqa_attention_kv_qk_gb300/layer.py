@@ -67,6 +67,8 @@ class DecodeLayer:
     cfg's rope_sections and rope_axes: rotary positions of several axes in packed steps
     (packed.pair_axes), rotation pairs per axis and their order, "blocks" or "cycle"."""
 
+    _shared = _Workspace()  # (replaced with the workspace)
+
     def __init__(self, cfg: dict, batch: int, capacity: int, device="cuda", page_size=None, block_table=None,
                  n_pages=None, max_q_len=1, cache=None, workspace=None, max_tokens=0):
         self.cfg = dict(cfg)
