@@ -68,6 +68,7 @@ class DecodeLayer:
     (packed.pair_axes), rotation pairs per axis and their order, "blocks" or "cycle"."""
 
     _shared = _Workspace()  # (replaced with the workspace)
+    _lens_unknown = False   # packed steps have run since the lengths were last known
 
     def __init__(self, cfg: dict, batch: int, capacity: int, device="cuda", page_size=None, block_table=None,
                  n_pages=None, max_q_len=1, cache=None, workspace=None, max_tokens=0):
@@ -237,12 +238,12 @@ class DecodeLayer:
         put(v, self.v_cache, self.v_scale)
         lens = torch.as_tensor(lens, dtype=torch.int32)
         self.seq_lens.copy_(lens)
-        self.max_len_hint = max(0, int(lens.max())) if lens.numel() else 0
+        self.max_len_hint, self._lens_unknown = max(0, int(lens.max())) if lens.numel() else 0, False
 
     def set_lengths(self, lens):
         lens = torch.as_tensor(lens, dtype=torch.int32)
         self.seq_lens.copy_(lens)
-        self.max_len_hint = max(0, int(lens.max())) if lens.numel() else 0
+        self.max_len_hint, self._lens_unknown = max(0, int(lens.max())) if lens.numel() else 0, False
 
     # ------------------------------------------------------------ calls
     def out_for(self, q_len: int, stream=None):
@@ -269,12 +270,16 @@ class DecodeLayer:
     def _bound(self, T, stream=None):
         """The bound on the lengths before a step of T tokens. max_len_hint grows with every
         step and knows nothing of rows that ended or went back to a shorter parent:
-        where the capacity would end by it, the lengths themselves are read (which waits
-        for the stream; not in a capture)."""
-        if self.max_len_hint + T > self.capacity and self.batch:
+        where the capacity would end by it, or after packed steps, the lengths themselves
+        are read (which waits for the stream). A capture does not read them: after packed steps
+        it goes by the longest that T tokens fit behind."""
+        if (self._lens_unknown or self.max_len_hint + T > self.capacity) and self.batch:
             with _memory_of(stream, self._index):
                 if not torch.cuda.is_current_stream_capturing():
                     self.max_len_hint = max(0, int(self.seq_lens.max()))
+                    self._lens_unknown = False
+                elif self._lens_unknown:
+                    self.max_len_hint = max(0, self.capacity - T)
         return self.max_len_hint
 
     def args(self, q, k_new, v_new, max_seq_len=None, q_rot=None, out=None) -> B.UaaStepArgs:
@@ -460,7 +465,8 @@ class DecodeLayer:
         output rows [n_tokens][Hq][D] go to `out` if given; rows behind the last request
         stay as they were, those of a request that is not served are zero. max_q_len: a
         bound on one request's tokens where the caller knows one (it chooses between
-        kernels)."""
+        kernels). The next step of equal lengths without max_seq_len reads the lengths, which
+        waits for the stream (in a capture it goes by the capacity)."""
         s = B.call_stream(stream, self._index)
         if out is None:
             out = self._packed_out.get(plan.n_tokens)
@@ -495,9 +501,9 @@ class DecodeLayer:
         return out
 
     def _packed_lengths(self):
-        """A packed step takes each request as far as the plan says, up to the capacity: the
-        bound that the next step of equal lengths goes by is read when it comes."""
-        self.max_len_hint = self.capacity
+        """A packed step, or a replay of it, takes each request as far as the plan says, up to the
+        capacity: the bound that the next step of equal lengths goes by is read when it comes."""
+        self.max_len_hint, self._lens_unknown = self.capacity, True
 
     def read_packed(self, plan, stream=None):
         """The cached keys and values of a plan's rows, [n_tokens][Hkv][D] in the layer's out

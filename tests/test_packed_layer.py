@@ -77,3 +77,42 @@ def test_attention_after_another_append(kv):
     alone.append_packed(*x, plan)
     b.step(torch.zeros((2, 8, 64), dtype=torch.bfloat16, device="cuda"), rows(2, 2), rows(2, 2))
     alone.attend_packed(plan, out)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f32"])
+def test_equal_steps_captured_after_a_packed_one(kv):
+    """The bound on the lengths is not known then: the capture goes by what fits the cache."""
+    cfg = dict(CFG, kv_dtype=kv)
+    s = make_step(cfg, [(30, 20), (0, 9), (120, 4)], 128, seed=4)
+    layer, plan = s["layer"], s["plan"]
+    x = rows(3, 8, 5), rows(3, 2, 6), rows(3, 2, 7)
+    layer.plan(s["q_lens"], plan)
+    layer.step_packed(s["q"], s["k"], s["v"], plan)
+    assert layer.seq_lens.tolist() == [50, 9, 124]
+    torch.cuda.synchronize()
+    graph, out = torch.cuda.CUDAGraph(), torch.zeros((3, 8, 64), device="cuda")
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        layer.step(*x, out=out)
+        layer.append(*x)
+        layer.partial()
+        layer.combine()
+    s.update(N=3, new=[1, 1, 1], q=x[0], k=x[1], v=x[2])
+    for lens in ([50, 9, 124], [52, 11, 126], [3, 0, 6]):
+        layer.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert layer.seq_lens.tolist() == [n + 2 for n in lens] and layer.device_status() == 0
+        s["lens"] = lens
+        check_out(cfg, out, expected(cfg, s)[0])
+        s["lens"] = [n + 1 for n in lens]
+        check_out(cfg, layer.out, expected(cfg, s)[0])
+    # a sequence without room is flagged, as ever
+    layer.seq_lens.copy_(torch.tensor([5, 128, 7], dtype=torch.int32))
+    graph.replay()
+    assert layer.device_status() == B.UAA_DEVFLAG_CAPACITY and layer.seq_lens.tolist() == [7, 128, 9]
+    # an eager step reads the lengths, and says so where there is no room
+    layer.plan(torch.tensor([1, 0, 1], dtype=torch.int32, device="cuda"), plan)
+    layer.step_packed(*(t.repeat(11, 1, 1) for t in x), plan)
+    with pytest.raises(B.UaaError, match="capacity"):
+        layer.step(*x)
