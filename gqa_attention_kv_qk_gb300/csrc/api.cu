@@ -1021,8 +1021,14 @@ struct PackedGeo {
     size_t total;
 };
 
-// Record rows of what the packed kernel cuts along the keys, at most.
+// Record rows of what the packed kernel cuts along the keys. A cut pair i of r_i rows in n_i pieces
+// has r_i n_i <= kMergeRows records for each kv head, and so all have at most
+// sum sqrt(kMergeRows r_i n_i) <= sqrt(kMergeRows R E), of R rows and E pieces together. E was below
+// 4.1 n_sm / Hkv where records were many (12,000 random batches); a pair without room stays whole, and
+// so do those beyond kPackedRecRows. 64 rows of 32 / 8 heads: 60 thousand records, 30 MiB at
+// head_dim 128, of which 13 were the most that was asked for.
 constexpr int kPackedRecRows = 320 << 10;
+constexpr int kPackedRecCutsPerSm = 5;
 
 // Entries of its work list beyond one for each row pair, per SM and over the kv heads. The
 // list (schedule.cuh) cuts the last m pairs, less than n_sm / Hkv + 1, at half an even share of what
@@ -1067,9 +1073,9 @@ uaa_status packed_geometry(const uaa_attn_desc* d, int batch, int n_tokens, int 
         l.pair_rows = pair_rows;
         l.max_pairs = (int)pairs;
         l.max_entries = (int)(pairs + cuts);
-        // no more record rows than the batch could cut into
-        const long long rows = 16LL * n_sm * (n_tokens * (long long)pl.G < pair_rows ? n_tokens * (long long)pl.G : pair_rows);
-        l.max_rec_rows = (int)(rows < kPackedRecRows ? rows : kPackedRecRows);
+        const double rec = d->n_kv_heads * ceil(sqrt((double)uaa::kMergeRows * n_tokens * pl.G *
+                                                     ((double)kPackedRecCutsPerSm * n_sm / d->n_kv_heads + 16)));
+        l.max_rec_rows = rec < kPackedRecRows ? (int)rec : kPackedRecRows;
         l.max_counters = 4 * n_sm + 16 * d->n_kv_heads;
         size_t at = g->total;
         auto take = [&at](size_t bytes) {

@@ -287,6 +287,7 @@ struct PackedParams {
 constexpr int kPackedRows = 256;
 constexpr int kPackedRows8 = 128;  // over 8-bit caches
 constexpr int kPackedKeys = 128;
+constexpr int kMergeRows = 2048;   // rows x pieces of a pair that one CTA merges, at most
 
 // One entry of its work list (schedule.cuh): piece `pieces & 0xffff` of `pieces >> 16` of
 // row pair rp of request b, for every kv head.

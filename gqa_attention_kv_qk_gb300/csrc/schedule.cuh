@@ -40,7 +40,6 @@ constexpr int kCostClasses = 16;
 constexpr int kCostFixed = 2;      // an item's start and end, in key blocks
 constexpr int kMinPieceBlocks = 2;
 constexpr int kMinGuided = 6;
-constexpr int kMergeRows = 2048;   // rows x pieces that one CTA merges
 constexpr int kSplitTries = 8;
 // Requests, and pairs, whose arrays lie in shared memory (others: the workspace's).
 constexpr int kScheduleFit = 512;

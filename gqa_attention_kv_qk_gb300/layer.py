@@ -63,7 +63,9 @@ class DecodeLayer:
     B.uaa_workspace_size bytes and more, zeroed once, or another layer's ws_tensor:
     layers whose steps run one after another share one (prefill chunks over a 4-bit
     cache take up to 512 MiB of it, or the widened rows of one sequence). max_tokens:
-    the most rows a packed step takes (step_packed; 0: none).
+    the most rows a packed step takes (step_packed; 0: none): their q rows and the parts of
+    what is cut along the keys add to the workspace (32 / 8 heads of 128: 15 MiB for 16
+    rows, 31 for 64, 136 for 1,024, 289 for 8,192), one more reason to share it.
     cfg's rope_sections and rope_axes: rotary positions of several axes in packed steps
     (packed.pair_axes), rotation pairs per axis and their order, "blocks" or "cycle"."""
 

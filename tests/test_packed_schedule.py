@@ -73,3 +73,16 @@ def test_many_long_requests_of_one_kv_head(kv, ragged):
         err = (out[i].double() - want).abs()
         worst, total = max(worst, float(err.max())), total + float(err.mean())
     assert worst <= 4e-3 and total / Bn <= 1e-4
+
+
+@pytest.mark.parametrize("n_tokens,mib", [(1, 6), (16, 16), (64, 32), (1024, 150), (8192, 300)])
+def test_workspace_grows_with_the_rows(n_tokens, mib):
+    """A decode step's workspace of 32 / 8 heads holds what its rows can be cut into, not what a full
+    batch's could (64 rows took 162 MiB)."""
+    d = B.make_desc(dict(n_q_heads=32, n_kv_heads=8, head_dim=128, kv_dtype="bf16", io_dtype="bf16", out_dtype="bf16"))
+    for batch in (1, 64):
+        size = B.uaa_packed_workspace_size(d, batch, n_tokens, 152)
+        assert 0 < size <= mib << 20
+        assert size >= n_tokens * 32 * 128 * 4
+    sizes = [B.uaa_packed_workspace_size(d, 64, n, 152) for n in (0, 1, 2, 63, 64, 65, 1000, 8192)]
+    assert sizes == sorted(sizes)
