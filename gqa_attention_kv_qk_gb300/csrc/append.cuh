@@ -7,17 +7,6 @@
 namespace uaa {
 namespace {
 
-// A queued near-boundary key pair (key_pair_exact): the element index of its cache
-// row, its position and rotation pair, the two elements' indices in the row, their
-// raw values, and the row's fp64 norm factor (0: no norm).
-struct StagedNear {
-    size_t slot;
-    double inv64;
-    int pos;
-    short ia, ib, pp, pad;
-    float ra, rb;
-};
-
 __device__ __forceinline__ void store8_f32(float* dst, const float (&y)[8], float scale)
 {
     reinterpret_cast<float4*>(dst)[0] = make_float4(y[0] * scale, y[1] * scale, y[2] * scale, y[3] * scale);
@@ -65,52 +54,11 @@ __device__ __forceinline__ float group_sum(float v)
 }
 
 template <int U>
-__device__ __forceinline__ double group_sum64(double v)
-{
-#pragma unroll
-    for (int o = U / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-template <int U>
 __device__ __forceinline__ float group_max(float v)
 {
 #pragma unroll
     for (int o = U / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
-}
-
-// A queued pair recomputed in fp64 and written over the cache's fp32 rounding.
-__device__ __forceinline__ void fix_staged_pair(const AppendParams& p, const StagedNear& q, const double* freq)
-{
-    const double wa = p.qk_norm ? static_cast<double>(p.k_norm_w[q.ia]) + p.norm_offset : 1.0;
-    const double wb = p.qk_norm ? static_cast<double>(p.k_norm_w[q.ib]) + p.norm_offset : 1.0;
-    __nv_bfloat16 ha, hb;
-    key_pair_exact(q.ra, q.rb, wa, wb, q.inv64, rope_cos_sin64(q.pp, p.half_rot, q.pos, freq[q.pp], p.mscale64), ha,
-                   hb);
-    static_cast<__nv_bfloat16*>(p.k_cache)[q.slot + q.ia] = ha;
-    static_cast<__nv_bfloat16*>(p.k_cache)[q.slot + q.ib] = hb;
-}
-
-// theta'_p / pi modulo 2 (exact) as a multiple of 2^-63, rounded to nearest: the
-// angle pos * theta'_p / pi modulo 2 is then the low 64 bits of pos * g, read as a
-// signed multiple of 2^-63 (an error below pos * 2^-64).
-__device__ __forceinline__ unsigned long long angle_step(double inv_freq_over_pi)
-{
-    return __double2ull_rn(ldexp(fmod(inv_freq_over_pi, 2.0), 63));
-}
-
-// cos and sin of pos * theta'_p times mscale, as rope_cos_sin computes them: the
-// angle in units of pi reduced to [-1, 1) and rounded once to fp32 for sincospif.
-// Here the reduction is exact integer arithmetic (no fp64 instruction): the
-// product's low 64 bits are the angle modulo 2, and the conversion rounds it to
-// nearest.
-__device__ __forceinline__ float2 rope_cos_sin_fx(int pos, unsigned long long g, float mscale)
-{
-    const long long t = static_cast<long long>(static_cast<unsigned long long>(pos) * g);
-    float sn, cn;
-    sincospif(__ll2float_rn(t) * 0x1p-63f, &sn, &cn);
-    return make_float2(cn * mscale, sn * mscale);
 }
 
 }  // namespace

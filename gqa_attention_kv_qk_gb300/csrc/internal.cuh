@@ -42,7 +42,7 @@ struct PackedRows {
     const int* axis_pos;       // [n_axes][n_tokens] rotary positions, or null: positions
     long long q_stride, k_stride, v_stride;  // elements between the rows of neighbouring tokens
     uint8_t pair_axis[kMaxHeadDim / 2];      // the axis that turns each pair
-    unsigned long long angle_step[kMaxHeadDim / 2];  // theta'_p / pi modulo 2 in units of 2^-63 (angle_step)
+    unsigned long long angle_step[kMaxHeadDim / 2];  // theta'_p / pi modulo 2 in units of 2^-63
 };
 
 struct AppendParams {
