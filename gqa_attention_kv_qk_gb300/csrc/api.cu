@@ -1040,8 +1040,8 @@ constexpr int kPackedCutsPerSm = 16;
 // Over 8-bit caches: query rows per kv head, where the caller bounds a request's tokens, up to
 // which the partial kernel takes the batch. Its warps widen codes in registers as they multiply,
 // but each unit of rows reads the cache anew. 64 requests of up to 8,000 tokens, vq8, head_dim 64 /
-// 128: 8 rows 94 / 154 us against 158 / 250 of the tcgen05 kernel, 16 rows 141 / 207 against 160 /
-// 250, 24 rows 185 / 271 against 160 / 250, 48 rows 271 / 409 against 163 / 253.
+// 128: 8 rows 89 / 149 us against 165 / 246 of the tcgen05 kernel, 16 rows 149 / 220 against 169 /
+// 246, 24 rows 185 / 271 against 171 / 250, 48 rows 271 / 409 against 181 / 254.
 constexpr int kPackedFewRows = 16;
 
 uaa_status packed_geometry(const uaa_attn_desc* d, int batch, int n_tokens, int q_len, int n_sm, PackedGeo* g)

@@ -15,10 +15,10 @@
 //
 // bf16 keys: cos, sin and a norm's factor are sums of two floats and the products exact, so that
 // the fp32 result is the nearest float to the exact one (97.7 % of all, the neighbour otherwise),
-// which is then rounded to bf16. Everything else takes norm and rotation in plain fp32. For
-// 16,200 normed tokens of 32 + 2 x 8 heads of 128 that took 121 us (4.9 TB/s) against 105 with keys
-// in plain fp32 too, whose bf16 rows then differ in one of some 10^4 elements; 8,191 tokens
-// without a norm take 60 us. The steps of equal lengths recompute in fp64 what lies near a
+// which is then rounded to bf16. Everything else takes norm and rotation in plain fp32. 16,200
+// normed tokens of 32 + 2 x 8 heads of 128 take 113 us (32 KiB a token: 4.7 TB/s), 8,191 tokens without
+// a norm 60 us (4.5 TB/s); with keys in plain fp32 too, whose bf16 rows then differ in one of some
+// 10^4 elements, the former took 105. The steps of equal lengths recompute in fp64 what lies near a
 // rounding boundary: the fp64 unit took 130 us of 236 here.
 #include "append.cuh"
 #include "schedule.cuh"

@@ -467,7 +467,8 @@ class DecodeLayer:
         output rows [n_tokens][Hq][D] go to `out` if given; rows behind the last request
         stay as they were, those of a request that is not served are zero. max_q_len: a
         bound on one request's tokens where the caller knows one (it chooses between
-        kernels). The next step of equal lengths without max_seq_len reads the lengths, which
+        kernels: single tokens over an 8-bit cache take up to three times as long without
+        max_q_len=1). The next step of equal lengths without max_seq_len reads the lengths, which
         waits for the stream (in a capture it goes by the capacity)."""
         s = B.call_stream(stream, self._index)
         if out is None:
