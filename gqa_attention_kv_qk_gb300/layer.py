@@ -506,7 +506,8 @@ class DecodeLayer:
     def _packed_lengths(self):
         """A packed step, or a replay of it, takes each request as far as the plan says, up to the
         capacity: the bound that the next step of equal lengths goes by is read when it comes."""
-        self.max_len_hint, self._lens_unknown = self.capacity, True
+        if self.batch:
+            self.max_len_hint, self._lens_unknown = self.capacity, True
 
     def read_packed(self, plan, stream=None):
         """The cached keys and values of a plan's rows, [n_tokens][Hkv][D] in the layer's out

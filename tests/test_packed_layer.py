@@ -116,3 +116,13 @@ def test_equal_steps_captured_after_a_packed_one(kv):
     layer.step_packed(*(t.repeat(11, 1, 1) for t in x), plan)
     with pytest.raises(B.UaaError, match="capacity"):
         layer.step(*x)
+
+
+def test_equal_steps_of_no_sequences_after_a_packed_one():
+    from gqa_attention_kv_qk_gb300.layer import DecodeLayer
+    from gqa_attention_kv_qk_gb300.packed import PackedPlan
+    layer, plan = DecodeLayer(CFG, 0, 128, max_tokens=4), PackedPlan(0, 4)
+    layer.plan(torch.zeros(0, dtype=torch.int32, device="cuda"), plan)
+    out = torch.full((4, 8, 64), 7.0, device="cuda")
+    layer.step_packed(rows(4, 8), rows(4, 2), rows(4, 2), plan, out=out)
+    assert bool((out == 7.0).all()) and tuple(layer.step(rows(0, 8), rows(0, 2), rows(0, 2)).shape) == (0, 8, 64)
