@@ -14,7 +14,7 @@
 // angles are reduced in 64-bit integers by steps from the host (rope_cos_sin_two).
 //
 // bf16 keys: cos, sin and a norm's factor are sums of two floats and the products exact, so that
-// the fp32 result is the nearest float to the exact one (97.7 % of all, the neighbour otherwise),
+// the fp32 result is the nearest float to the exact one, or now and then its neighbour,
 // which is then rounded to bf16. Everything else takes norm and rotation in plain fp32. 16,200
 // normed tokens of 32 + 2 x 8 heads of 128 take 113 us (32 KiB a token: 4.7 TB/s), 8,191 tokens without
 // a norm 60 us (4.5 TB/s); with keys in plain fp32 too, whose bf16 rows then differ in one of some
